@@ -88,7 +88,7 @@ def draw(rng):
             case["room"] = rng.randrange(0, 200)
         return case
     s = log(1, 24)
-    ctx = log(16, min(32768, 170000 // s // max(1, hkv // 8)))
+    ctx = log(16, min(32768, 155000 // s // max(1, hkv // 8)))
     least = max(1, int(ctx * rng.choice([0.1, 0.6, 1.0])))
     if op == "decode_weights":
         return dict(op=op, seqs=s, ctx=ctx, least=least, heads=h, kv_heads=hkv, head_dim=d,
