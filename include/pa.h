@@ -14,6 +14,9 @@
  * pa_decode_multi (several query tokens per sequence: chunked prefill,
  * speculative verification), and pa_decode_grouped, pa_decode for groups of sequences that share blocks
  * (beams, parallel samples), which reads each shared block once per group.
+ * Around them: pa_rope_append (rotary positions fused with the append), pa_prefill
+ * (attention over whole prompts), pa_prefill_weights / pa_decode_weights (the attention
+ * each token received) and pa_evict (eviction by it).
  *
  * Sources for what each call computes (page title, section):
  *   [P1] "PagedAttention：大模型推理性能优化的核心技术解析" (bmjup.com),
@@ -480,6 +483,186 @@ int pa_decode_noalloc(void* out, const void* q, const void* k_cache, const void*
                       const int32_t* context_lens, int32_t max_context_len,
                       int32_t num_seqs, int32_t num_heads, float scale,
                       const pa_cache_desc* cache, int32_t partition_size, void* stream);
+
+/*
+ * Rotary positions, prompt attention and eviction: the calls of a serving step
+ * around pa_decode.
+ *
+ *   pa_rope_append       rotate q and k by their positions, append k and v
+ *   pa_prefill           causal attention over whole packed prompts
+ *   pa_prefill_weights   attention weight each prompt token received
+ *   pa_decode_weights    pa_decode that also adds each token's weight
+ *   pa_evict             keep a budget of tokens per kv head, compact the rest away
+ *
+ * Token strides. q, k and v of these calls are [num_tokens][heads][head_dim] with
+ * head_dim and heads contiguous and any distance between tokens (in elements, a
+ * multiple of 16 bytes, at least heads * head_dim): slices of a packed projection need
+ * no copy. Outputs are contiguous.
+ */
+
+/*
+ * pa_rope_desc — how positions turn pairs of a q or k row (rotary position
+ * embedding: Su et al., "RoFormer: Enhanced Transformer with Rotary Position
+ * Embedding"). Frequency i < rotary_dim / 2 turns the pair (x_a, x_b) by
+ *     theta_i = positions[axis[i]][token] * inv_freq[i]
+ *     (x_a, x_b) -> mscale * (x_a cos theta_i - x_b sin theta_i,
+ *                             x_b cos theta_i + x_a sin theta_i)
+ * with (a, b) = (i, i + rotary_dim / 2) for PA_ROPE_HALF and (2i, 2i + 1) for
+ * PA_ROPE_ADJACENT. Elements from rotary_dim on are copied unchanged. Text has one
+ * axis; images and video give each token a position per axis (time, height, width)
+ * and axis[i] says which one frequency i follows.
+ */
+#define PA_ROPE_HALF 0
+#define PA_ROPE_ADJACENT 1
+#define PA_ROPE_MAX_AXES 4
+typedef struct pa_rope_desc {
+    int32_t rotary_dim;   /* a multiple of 16 in [16, head_dim]              */
+    int32_t pairs;        /* PA_ROPE_HALF or PA_ROPE_ADJACENT                */
+    int32_t num_axes;     /* 1 .. PA_ROPE_MAX_AXES                           */
+    float mscale;         /* factor of the turned pairs (1 for plain rotary) */
+    double inv_freq[64];  /* radians per position, rotary_dim / 2 entries    */
+    uint8_t axis[64];     /* axis of each frequency, below num_axes          */
+} pa_rope_desc;
+
+/*
+ * pa_rope_append — q_out = rotated q; rotated k, and v as it is, into their cache
+ * slots (pa_kv_append's slots and rules; a padding token's q is rotated too).
+ *
+ *   q_out         device, [num_tokens][num_heads][head_dim], contiguous; must not
+ *                 overlap q, k or v (PA_ERR_INVALID_ARG).
+ *   q, k, v       device, the cache's type, token strides as above.
+ *   positions     device, int32 [num_axes][num_tokens]; any value, negative too.
+ *   slot_mapping  device, int64 [num_tokens].
+ * The angle is reduced exactly in 64-bit fixed point, so positions of any size keep
+ * the full fp32 accuracy of the sine and cosine. num_heads >= 0: with 0 only k and v
+ * are appended (q and q_out may then be NULL).
+ *
+ * pa_rope_append_quant — the same into a quantised cache: q, k, v and q_out bf16, each
+ * k and v element stored as the code of (its unrounded fp32 value) / scale[kv head].
+ */
+int pa_rope_append(void* q_out, const void* q, const void* k, const void* v, int64_t q_stride,
+                   int64_t k_stride, int64_t v_stride, const int32_t* positions,
+                   const int64_t* slot_mapping, int32_t num_tokens, int32_t num_heads,
+                   void* k_cache, void* v_cache, const pa_cache_desc* cache,
+                   const pa_rope_desc* rope, void* stream);
+int pa_rope_append_quant(void* q_out, const void* q, const void* k, const void* v,
+                         int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                         const int32_t* positions, const int64_t* slot_mapping,
+                         int32_t num_tokens, int32_t num_heads, void* k_cache, void* v_cache,
+                         const float* k_scale, const float* v_scale, const pa_cache_desc* cache,
+                         const pa_rope_desc* rope, void* stream);
+
+/*
+ * pa_prefill — causal attention over whole prompts, packed one after another: prompt
+ * s holds the rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 of q, k, v and out, and its
+ * row i attends to its rows 0 .. i:
+ *     out[i][h] = softmax_{t <= i}(scale * q[i][h] . k[t][kh]) . v[..][kh]
+ *     lse[h][i] = ln sum_{t <= i} exp(scale * q[i][h] . k[t][kh])
+ * with kh = h / (num_heads / num_kv_heads): [P3 § 显存消耗的三大来源]'s attention for
+ * every query of the prompt at once, before its K and V are only read from the pool.
+ *
+ *   q, k, v       device, PA_F32 or PA_BF16, head_dim 64 or 128, token strides as above.
+ *   out           device, [total_tokens][num_heads][head_dim]; must not overlap the
+ *                 inputs.
+ *   lse           device, float [num_heads][total_tokens], or NULL.
+ *   cu_seqlens    device, int32 [num_seqs + 1], non-decreasing, in [0, total_tokens].
+ *                 A prompt may be empty. Rows of no prompt (before the first, behind
+ *                 the last) are neither read as keys nor written.
+ *   max_seq_len   host bound on a prompt's length. A prompt with bad bounds or a
+ *                 longer one is skipped and recorded as PA_ERR_BAD_INDEX.
+ * A query's result depends on its own prompt's rows 0 .. i alone, bit for bit, whatever
+ * the other rows hold (infinities and NaN too) and whatever else is in the call.
+ * bf16: products on the tensor cores with fp32 sums; the softmax weights are rounded to
+ * bf16 for the second product. fp32: fp32 throughout.
+ */
+int pa_prefill(void* out, const void* q, const void* k, const void* v, int64_t q_stride,
+               int64_t k_stride, int64_t v_stride, const int32_t* cu_seqlens, int32_t num_seqs,
+               int32_t total_tokens, int32_t max_seq_len, int32_t num_heads,
+               int32_t num_kv_heads, int32_t head_dim, int32_t dtype, float scale, float* lse,
+               void* stream);
+
+/*
+ * pa_prefill_weights — the attention weight each token of a prompt received:
+ *     weights[s][kh][t] = sum over the heads h of kv head kh and the queries i >= t of
+ *                         exp(scale * q[i][h] . k[t][kh] - lse[h][i])
+ * with lse as pa_prefill returned it. last_queries > 0 restricts the sum to the last
+ * that many queries of each prompt (an observation window); 0 takes every query.
+ *
+ *   weights       device, float [num_seqs][num_kv_heads][weights_stride], written
+ *                 whole: zeros from the prompt's length on, and for a skipped prompt.
+ *   weights_stride  at least max_seq_len.
+ * Other arguments and rules as pa_prefill. The sums are fp32 in a fixed order.
+ */
+int pa_prefill_weights(float* weights, int64_t weights_stride, const void* q, const void* k,
+                       int64_t q_stride, int64_t k_stride, const float* lse,
+                       const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                       int32_t max_seq_len, int32_t num_heads, int32_t num_kv_heads,
+                       int32_t head_dim, int32_t dtype, float scale, int32_t last_queries,
+                       void* stream);
+
+/*
+ * pa_decode_weights — pa_decode (the same out, bit for bit) that also adds the step's
+ * softmax weights to the tokens' running totals:
+ *     weights[s][kh][t] += sum over the heads h of kv head kh of
+ *                          softmax_t(scale * q[s][h] . K_t)        t < context_lens[s]
+ *   weights       device, float [num_seqs][num_kv_heads][weights_stride]; entries from
+ *                 the context's length on are left as they are.
+ *   weights_stride  at least max_context_len.
+ *   workspace     at least pa_decode_weights_workspace_size(...) bytes: pa_decode's, and
+ *                 one fp32 score per (sequence, head, token).
+ * pa_decode_weights_quant — the same over a quantised cache (pa_decode_quant's arguments).
+ * Tokens behind a block id outside the pool get no weight.
+ */
+int pa_decode_weights(void* out, float* weights, int64_t weights_stride, const void* q,
+                      const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                      int32_t block_table_stride, const int32_t* context_lens,
+                      int32_t max_context_len, int32_t num_seqs, int32_t num_heads, float scale,
+                      const pa_cache_desc* cache, int32_t partition_size, void* workspace,
+                      size_t workspace_bytes, void* stream);
+int pa_decode_weights_quant(void* out, float* weights, int64_t weights_stride, const void* q,
+                            const void* k_cache, const void* v_cache, const float* k_scale,
+                            const float* v_scale, const int32_t* block_tables,
+                            int32_t block_table_stride, const int32_t* context_lens,
+                            int32_t max_context_len, int32_t num_seqs, int32_t num_heads,
+                            float scale, const pa_cache_desc* cache, int32_t partition_size,
+                            void* workspace, size_t workspace_bytes, void* stream);
+size_t pa_decode_weights_workspace_size(int32_t num_seqs, int32_t num_heads,
+                                        int32_t max_context_len, const pa_cache_desc* cache,
+                                        int32_t partition_size);
+
+/*
+ * pa_evict — shrink every context above `budget` tokens to `budget`, per kv head: keep
+ * the `recent` last tokens and, of the others, the budget - recent with the largest
+ * weights (ties: the lowest position; NaN counts as -infinity), and move the kept rows
+ * of both caches to the positions 0 .. budget - 1 of the same block table. (The few
+ * tokens that receive most of the attention are the ones to keep: Zhang et al., "H2O:
+ * Heavy-Hitter Oracle for Efficient Generative Inference of Large Language Models".)
+ *
+ * With edge = budget - recent: a kept token that lies below edge stays; the others of the
+ * heaviest, in order, fill the positions below edge whose tokens go, in order; the recent
+ * tokens follow at edge .. budget - 1. Attention does not depend on the order of the
+ * cached tokens, and their keys keep the rotation of their original positions (the next
+ * token's position is still the caller's count, not the new length).
+ *
+ *   weights       device, float [num_seqs][num_kv_heads][weights_stride].
+ *   weights_out   the weights after the move: kept[..][j]'s weight at j, zeros from the
+ *                 new length to weights_stride. May be `weights` itself.
+ *   new_context_lens  device, int32 [num_seqs]: min(n, budget); not context_lens itself.
+ *   kept          device, int32 [num_seqs][num_kv_heads][budget]: the old position of
+ *                 the token now at j; for a context within the budget j itself, then -1.
+ *   budget >= 1, 0 <= recent <= budget, weights_stride >= max(max_context_len, budget).
+ * Any cache type. max_context_len up to pa_evict_max_context() (PA_ERR_UNSUPPORTED). The
+ * blocks of one call's sequences must be distinct: a block shared by reference count has to
+ * be copied first (pa_block_copy). Blocks past ceil(budget / block_size) are free
+ * afterwards. A row behind a block id outside the pool is neither read nor written
+ * (PA_ERR_BAD_INDEX).
+ */
+int pa_evict(void* k_cache, void* v_cache, const int32_t* block_tables,
+             int32_t block_table_stride, const int32_t* context_lens, int32_t max_context_len,
+             int32_t num_seqs, const float* weights, float* weights_out, int64_t weights_stride,
+             int32_t* new_context_lens, int32_t* kept, int32_t budget, int32_t recent,
+             const pa_cache_desc* cache, void* stream);
+int pa_evict_max_context(void);
 
 /*
  * pa_sync_check — wait for `stream`, then read and clear the current device's

@@ -65,6 +65,17 @@ class pa_cache_desc(ctypes.Structure):
                 ("dtype", ctypes.c_int32)]
 
 
+PA_ROPE_HALF = 0            # pairs (i, i + rotary_dim / 2)
+PA_ROPE_ADJACENT = 1        # pairs (2i, 2i + 1)
+PA_ROPE_MAX_AXES = 4
+
+
+class pa_rope_desc(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("pairs", ctypes.c_int32),
+                ("num_axes", ctypes.c_int32), ("mscale", ctypes.c_float),
+                ("inv_freq", ctypes.c_double * 64), ("axis", ctypes.c_uint8 * 64)]
+
+
 def _status_name(code: int) -> str:
     try:
         return load_library().pa_status_string(code).decode()
@@ -113,6 +124,24 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.pa_decode_multi_quant.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32,
                                               i32, i32, i32, f32, desc, i32, vp, sz, vp]
         lib.pa_block_swap.argtypes = [vp, i32, vp, vp, desc, vp, vp, desc, vp]
+        i64, rope = ctypes.c_int64, ctypes.POINTER(pa_rope_desc)
+        lib.pa_rope_append.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, vp, i32, i32, vp, vp,
+                                       desc, rope, vp]
+        lib.pa_rope_append_quant.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, vp, i32, i32, vp,
+                                             vp, vp, vp, desc, rope, vp]
+        lib.pa_prefill.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, i32, i32, i32, i32, i32, i32,
+                                   i32, f32, vp, vp]
+        lib.pa_prefill_weights.argtypes = [vp, i64, vp, vp, i64, i64, vp, vp, i32, i32, i32, i32,
+                                           i32, i32, i32, f32, i32, vp]
+        lib.pa_decode_weights.argtypes = [vp, vp, i64, vp, vp, vp, vp, i32, vp, i32, i32, i32, f32,
+                                          desc, i32, vp, sz, vp]
+        lib.pa_decode_weights_quant.argtypes = [vp, vp, i64, vp, vp, vp, vp, vp, vp, i32, vp, i32,
+                                                i32, i32, f32, desc, i32, vp, sz, vp]
+        lib.pa_decode_weights_workspace_size.argtypes = [i32, i32, i32, desc, i32]
+        lib.pa_decode_weights_workspace_size.restype = sz
+        lib.pa_evict.argtypes = [vp, vp, vp, i32, vp, i32, i32, vp, vp, i64, vp, vp, i32, i32, desc,
+                                 vp]
+        lib.pa_evict_max_context.argtypes = []
         lib.pa_sync_check.argtypes = [vp]
         lib.pa_stream_read.argtypes = [vp, sz, vp, i32, vp]
         lib.pa_test_skip_load.argtypes = [i32]
@@ -586,6 +615,250 @@ def pa_decode_noalloc(out, q, k_cache, v_cache, block_tables, context_lens, scal
         float(scale), ctypes.byref(desc), int(partition_size), _stream(stream)))
 
 
+# ---------------------------------------------------------------------------
+# the calls around decode: rotary append, prompt attention, weights, eviction
+# ---------------------------------------------------------------------------
+def rope_desc(rotary_dim: int, base: float = 10000.0, inv_freq=None, sections=None,
+              pairs: str = "half", mscale: float = 1.0) -> pa_rope_desc:
+    """How positions turn pairs: ``inv_freq`` holds rotary_dim / 2 radians per position
+    (default base ** (-2 i / rotary_dim)); ``sections`` the number of frequencies that
+    follow each axis, in order (default: one axis); ``pairs`` "half" (i, i + rotary_dim / 2)
+    or "adjacent" (2i, 2i + 1)."""
+    half = rotary_dim // 2
+    if rotary_dim % 2 or not 0 < half <= 64:
+        raise ValueError("rotary_dim must be even, in [2, 128]")
+    if inv_freq is None:
+        inv_freq = [base ** (-2.0 * i / rotary_dim) for i in range(half)]
+    sections = [half] if sections is None else [int(x) for x in sections]
+    if len(inv_freq) != half or sum(sections) != half or min(sections) < 0:
+        raise ValueError("inv_freq needs rotary_dim / 2 entries, and sections that sum")
+    if pairs not in ("half", "adjacent"):
+        raise ValueError('pairs must be "half" or "adjacent"')
+    d = pa_rope_desc(rotary_dim, PA_ROPE_HALF if pairs == "half" else PA_ROPE_ADJACENT,
+                     len(sections), mscale)
+    axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    for i in range(half):
+        d.inv_freq[i], d.axis[i] = float(inv_freq[i]), axis[i]
+    return d
+
+
+def _rows(t, name: str, dtype):
+    """Pointer and token stride of a [tokens][heads][head_dim] tensor whose heads and
+    head_dim are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    _on_current_device(t, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    n, h, d = (int(x) for x in t.shape)
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name} must be contiguous in heads and head_dim")
+    return ctypes.c_void_p(t.data_ptr()), int(t.stride(0)) if n > 1 else h * d
+
+
+def _rope_call(entry, scales, q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, rope,
+               dtype, stream):
+    torch = _torch()
+    _same_pool(k_cache, v_cache)
+    desc = cache_desc(k_cache)
+    t = int(slot_mapping.shape[0])
+    if (k.dim() != 3 or tuple(k.shape) != (t, desc.num_kv_heads, desc.head_dim)
+            or k.shape != v.shape):
+        raise ValueError("k and v must be [num_tokens][num_kv_heads][head_dim]")
+    if q.dim() != 3 or q.shape[0] != t or q.shape[2] != desc.head_dim or q_out.shape != q.shape:
+        raise ValueError("q and q_out must be [num_tokens][num_heads][head_dim]")
+    if tuple(positions.shape) != (rope.num_axes, t):
+        raise ValueError("positions must be [num_axes][num_tokens]")
+    if q_out.dtype != dtype:
+        raise TypeError(f"q_out must be {dtype}, got {q_out.dtype}")
+    for x in scales:
+        if tuple(x.shape) != (desc.num_kv_heads,):
+            raise ValueError("k_scale and v_scale must be [num_kv_heads]")
+    (qp, qs), (kp, ks), (vp, vs) = (_rows(x, n, dtype) for x, n in ((q, "q"), (k, "k"), (v, "v")))
+    _check(entry(
+        _dev(q_out, "q_out"), qp, kp, vp, qs, ks, vs, _dev(positions, "positions", torch.int32),
+        _dev(slot_mapping, "slot_mapping", torch.int64), t, int(q.shape[1]),
+        _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+        *(_dev(x, "scale", torch.float32) for x in scales), ctypes.byref(desc),
+        ctypes.byref(rope), _stream(stream)))
+
+
+def pa_rope_append(q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, rope,
+                   stream=None) -> None:
+    """q_out = q turned by its positions; k turned likewise and v as it is go to their
+    cache slots (int64; <0: padding, not stored). q, k, v [T][heads][head_dim] may be
+    slices of a packed projection; positions int32 [num_axes][T]; ``rope`` from
+    ``rope_desc``."""
+    _rope_call(load_library().pa_rope_append, (), q_out, q, k, v, positions, slot_mapping, k_cache,
+               v_cache, rope, k_cache.dtype, stream)
+
+
+def pa_rope_append_quant(q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, k_scale,
+                         v_scale, rope, stream=None) -> None:
+    """pa_rope_append into a float8_e4m3fn or int8 code pool (q, k, v, q_out bfloat16;
+    codes of value / scale[kv head])."""
+    _rope_call(load_library().pa_rope_append_quant, (k_scale, v_scale), q_out, q, k, v, positions,
+               slot_mapping, k_cache, v_cache, rope, _torch().bfloat16, stream)
+
+
+def _prompt_shapes(q, k, cu_seqlens, max_seq_len):
+    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        raise ValueError("q must be [total_tokens][num_heads][head_dim], k and v "
+                         "[total_tokens][num_kv_heads][head_dim]")
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be [num_seqs + 1]")
+    s = int(cu_seqlens.shape[0]) - 1
+    if max_seq_len is None:
+        max_seq_len = int((cu_seqlens[1:] - cu_seqlens[:-1]).max().item()) if s else 0
+    return s, int(max_seq_len)
+
+
+def pa_prefill(out, q, k, v, cu_seqlens, scale: float, max_seq_len: int | None = None, lse=None,
+               stream=None) -> None:
+    """Causal attention over whole packed prompts: rows cu_seqlens[s] .. cu_seqlens[s+1] - 1
+    of q / out [T][H][D] and k, v [T][Hkv][D] are prompt s. ``lse`` (float32 [H][T]) gets the
+    log-sum-exp. ``max_seq_len`` is a host bound on the prompts' lengths (computed with a
+    device sync if omitted)."""
+    torch = _torch()
+    s, max_seq_len = _prompt_shapes(q, k, cu_seqlens, max_seq_len)
+    if out.shape != q.shape or v.shape != k.shape:
+        raise ValueError("out must have q's shape and v k's")
+    t, h, d = (int(x) for x in q.shape)
+    if out.dtype != q.dtype:
+        raise TypeError(f"out must be {q.dtype}, got {out.dtype}")
+    if lse is not None and tuple(lse.shape) != (h, t):
+        raise ValueError("lse must be [num_heads][total_tokens]")
+    (qp, qs), (kp, ks), (vp, vs) = (_rows(x, n, q.dtype) for x, n in ((q, "q"), (k, "k"), (v, "v")))
+    _check(load_library().pa_prefill(
+        _dev(out, "out"), qp, kp, vp, qs, ks, vs, _dev(cu_seqlens, "cu_seqlens", torch.int32), s, t,
+        max_seq_len, h, int(k.shape[1]), d, _dtype_code(q), float(scale),
+        ctypes.c_void_p(0) if lse is None else _dev(lse, "lse", torch.float32), _stream(stream)))
+
+
+def pa_prefill_weights(weights, q, k, lse, cu_seqlens, scale: float,
+                       max_seq_len: int | None = None, last_queries: int = 0,
+                       stream=None) -> None:
+    """weights[s][kh][t] (float32 [S][Hkv][>= max_seq_len], written whole) = the softmax weight
+    prompt token t received, summed over the heads of kv head kh and the prompt's queries (its
+    last ``last_queries`` ones if > 0). ``lse`` as pa_prefill returned it."""
+    torch = _torch()
+    s, max_seq_len = _prompt_shapes(q, k, cu_seqlens, max_seq_len)
+    t, h, d = (int(x) for x in q.shape)
+    if weights.dim() != 3 or tuple(weights.shape[:2]) != (s, int(k.shape[1])):
+        raise ValueError("weights must be [num_seqs][num_kv_heads][weights_stride]")
+    if tuple(lse.shape) != (h, t):
+        raise ValueError("lse must be [num_heads][total_tokens]")
+    (qp, qs), (kp, ks) = _rows(q, "q", q.dtype), _rows(k, "k", q.dtype)
+    _check(load_library().pa_prefill_weights(
+        _dev(weights, "weights", torch.float32), int(weights.shape[2]), qp, kp, qs, ks,
+        _dev(lse, "lse", torch.float32), _dev(cu_seqlens, "cu_seqlens", torch.int32), s, t,
+        max_seq_len, h, int(k.shape[1]), d, _dtype_code(q), float(scale), int(last_queries),
+        _stream(stream)))
+
+
+def pa_decode_weights_workspace_size(num_seqs: int, num_heads: int, max_context_len: int, k_cache,
+                                     partition_size: int = 0) -> int:
+    lib = load_library()
+    desc = cache_desc(k_cache)
+    n = lib.pa_decode_weights_workspace_size(num_seqs, num_heads, max_context_len,
+                                             ctypes.byref(desc), partition_size)
+    if n == 0:
+        msg = lib.pa_get_last_error().decode()
+        rc = _num_partitions(num_seqs, num_heads, max_context_len, desc, 1, partition_size)
+        if rc < 0:
+            raise PAError(rc, msg)
+    return int(n)
+
+
+def _decode_weights_call(entry, scales, out, weights, q, k_cache, v_cache, block_tables,
+                         context_lens, scale, dtype, max_context_len, partition_size, workspace,
+                         stream):
+    torch = _torch()
+    _same_pool(k_cache, v_cache)
+    desc = cache_desc(k_cache)
+    s, h, d = (int(x) for x in q.shape)
+    if tuple(out.shape) != (s, h, d) or d != desc.head_dim:
+        raise ValueError("q and out must be [num_seqs][num_heads][head_dim]")
+    if q.dtype != dtype or out.dtype != dtype:
+        raise TypeError(f"q and out must be {dtype}")
+    if block_tables.dim() != 2 or block_tables.shape[0] != s or context_lens.shape != (s,):
+        raise ValueError("block_tables must be [num_seqs][stride], context_lens [num_seqs]")
+    if weights.dim() != 3 or tuple(weights.shape[:2]) != (s, desc.num_kv_heads):
+        raise ValueError("weights must be [num_seqs][num_kv_heads][weights_stride]")
+    for x in scales:
+        if tuple(x.shape) != (desc.num_kv_heads,):
+            raise ValueError("k_scale and v_scale must be [num_kv_heads]")
+    if max_context_len is None:
+        max_context_len = int(context_lens.max().item()) if s else 0
+    need = pa_decode_weights_workspace_size(s, h, max_context_len, k_cache, partition_size)
+    ws_ptr, ws_bytes = _quant_ws(need, workspace, q.device)
+    _check(entry(
+        _dev(out, "out"), _dev(weights, "weights", torch.float32), int(weights.shape[2]),
+        _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+        *(_dev(x, "scale", torch.float32) for x in scales),
+        _dev(block_tables, "block_tables", torch.int32), int(block_tables.shape[1]),
+        _dev(context_lens, "context_lens", torch.int32), int(max_context_len), s, h, float(scale),
+        ctypes.byref(desc), int(partition_size), ws_ptr, ws_bytes, _stream(stream)))
+
+
+def pa_decode_weights(out, weights, q, k_cache, v_cache, block_tables, context_lens, scale: float,
+                      max_context_len: int | None = None, partition_size: int = 0, workspace=None,
+                      stream=None) -> None:
+    """pa_decode that also adds the step's softmax weights to ``weights`` (float32
+    [S][Hkv][>= max_context_len]), summed over the query heads of each kv head. ``workspace``:
+    ``pa_decode_weights_workspace_size`` bytes (allocated here if omitted)."""
+    _decode_weights_call(load_library().pa_decode_weights, (), out, weights, q, k_cache, v_cache,
+                         block_tables, context_lens, scale, k_cache.dtype, max_context_len,
+                         partition_size, workspace, stream)
+
+
+def pa_decode_weights_quant(out, weights, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                            context_lens, scale: float, max_context_len: int | None = None,
+                            partition_size: int = 0, workspace=None, stream=None) -> None:
+    """pa_decode_weights over a quantised pool (pa_decode_quant's arguments)."""
+    _decode_weights_call(load_library().pa_decode_weights_quant, (k_scale, v_scale), out, weights,
+                         q, k_cache, v_cache, block_tables, context_lens, scale,
+                         _torch().bfloat16, max_context_len, partition_size, workspace, stream)
+
+
+def pa_evict(k_cache, v_cache, block_tables, context_lens, weights, weights_out, new_context_lens,
+             kept, budget: int, recent: int, max_context_len: int | None = None,
+             stream=None) -> None:
+    """Shrink every context above ``budget`` tokens to ``budget`` per kv head: keep the
+    ``recent`` last tokens and the heaviest others by ``weights`` (float32 [S][Hkv][stride]),
+    moved in both caches to positions 0 .. budget - 1 of the same block table.
+
+    ``weights_out`` (may be ``weights``) gets the moved weights, ``new_context_lens`` (int32
+    [S]) the new lengths, ``kept`` (int32 [S][Hkv][budget]) the old position of the token now
+    at each place. The sequences must not share blocks."""
+    torch = _torch()
+    _same_pool(k_cache, v_cache)
+    desc = cache_desc(k_cache)
+    s = int(context_lens.shape[0])
+    if block_tables.dim() != 2 or block_tables.shape[0] != s or new_context_lens.shape != (s,):
+        raise ValueError("block_tables [S][stride], context_lens [S], new_context_lens [S]")
+    if (weights.dim() != 3 or tuple(weights.shape[:2]) != (s, desc.num_kv_heads)
+            or weights_out.shape != weights.shape):
+        raise ValueError("weights and weights_out must be [num_seqs][num_kv_heads][stride]")
+    if tuple(kept.shape) != (s, desc.num_kv_heads, int(budget)):
+        raise ValueError("kept must be [num_seqs][num_kv_heads][budget]")
+    if max_context_len is None:
+        max_context_len = int(context_lens.max().item()) if s else 0
+    _check(load_library().pa_evict(
+        _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+        _dev(block_tables, "block_tables", torch.int32), int(block_tables.shape[1]),
+        _dev(context_lens, "context_lens", torch.int32), int(max_context_len), s,
+        _dev(weights, "weights", torch.float32), _dev(weights_out, "weights_out", torch.float32),
+        int(weights.shape[2]), _dev(new_context_lens, "new_context_lens", torch.int32),
+        _dev(kept, "kept", torch.int32), int(budget), int(recent), ctypes.byref(desc),
+        _stream(stream)))
+
+
+def pa_evict_max_context() -> int:
+    """Longest context pa_evict takes."""
+    return int(load_library().pa_evict_max_context())
+
+
 def pa_set_grouped_consumer(consumer: int) -> int:
     """Select the grouped / multi-token consumer (PA_GROUPED_MMA_SYNC or
     PA_GROUPED_TCGEN05); returns the previous one. Process-wide."""
@@ -603,6 +876,9 @@ __all__ = ["pa_kv_append", "pa_decode", "pa_decode_noalloc", "pa_block_copy", "p
            "pa_decode_num_partitions", "pa_decode_grouped", "pa_decode_grouped_workspace_size",
            "pa_decode_grouped_num_partitions", "pa_decode_multi", "pa_decode_multi_workspace_size",
            "pa_decode_multi_num_partitions", "pa_kv_append_quant", "pa_decode_quant", "pa_block_swap",
-           "pa_set_grouped_consumer",
+           "pa_set_grouped_consumer", "rope_desc", "pa_rope_desc", "pa_rope_append",
+           "pa_rope_append_quant", "pa_prefill", "pa_prefill_weights", "pa_decode_weights",
+           "pa_decode_weights_quant", "pa_decode_weights_workspace_size", "pa_evict",
+           "pa_evict_max_context",
            "pa_sync_check", "pa_cache_desc", "cache_desc",
            "load_library", "header_functions", "PAError"]

@@ -123,6 +123,31 @@ class BlockManager:
         seq.length = pos + 1
         return seq.table[j] * self.block_size + off
 
+    def unshare(self, seq: Sequence) -> int:
+        """Replace every block of ``seq`` that others still reference by a private copy, as
+        rows about to move inside it require (``pa_evict``); the (src, dst) pairs are recorded
+        in ``self.copies``. Returns how many."""
+        shared = [j for j, b in enumerate(seq.table) if self.refcount[b] > 1]
+        if len(shared) > self.num_free:
+            raise PoolExhausted(f"{len(shared)} shared blocks to copy, {self.num_free} free")
+        for j in shared:
+            b, nb = seq.table[j], self.allocate()
+            self.copies.append((b, nb))
+            self.refcount[b] -= 1
+            seq.table[j] = nb
+        return len(shared)
+
+    def truncate(self, seq: Sequence, length: int) -> None:
+        """Keep the first ``length`` positions (after ``pa_evict``): blocks behind them are
+        released."""
+        if not 0 <= length <= seq.length:
+            raise ValueError(f"length {length} outside [0, {seq.length}]")
+        keep = -(-length // self.block_size)
+        for b in seq.table[keep:]:
+            self._release(b)
+        del seq.table[keep:]
+        seq.length = length
+
     def take_copies(self) -> np.ndarray:
         """Copy pairs recorded since the last call, as int64 [P][2]."""
         pairs = np.asarray(self.copies, dtype=np.int64).reshape(-1, 2)

@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -152,6 +153,26 @@ struct Plan {
 
 int round_up16(int x) { return (x + 15) / 16 * 16; }
 
+// Distance between tokens (elements of e bytes) of a tensor whose token holds `row`.
+int check_stride(const char* name, int64_t stride, int64_t row, int e) {
+    if (stride < row)
+        return fail(PA_ERR_INVALID_ARG, "token stride %lld of %s below its %lld elements per token",
+                    (long long)stride, name, (long long)row);
+    if (stride * e % 16 != 0 || stride > (INT64_C(1) << 36))
+        return fail(PA_ERR_ALIGN, "token stride %lld of %s must be a multiple of 16 bytes below 2^36",
+                    (long long)stride, name);
+    return PA_OK;
+}
+
+size_t strided_bytes(int64_t tokens, int64_t stride, int64_t row, int e) {
+    return tokens > 0 ? (size_t)((tokens - 1) * stride + row) * e : 0;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
+    return na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
+
 // Partition policy: split the context only when the (sequence, head) work
 // units alone cannot fill the GPU, then into 512-token partitions.
 // num_query_tokens >= 0 selects the multi-token mode (pa_decode_multi): query
@@ -295,6 +316,23 @@ int plan_decode(int32_t num_seqs, int32_t num_heads, int32_t max_ctx, const pa_c
     return PA_OK;
 }
 
+// Workspace of pa_decode_weights: pa_decode's, then the scores [S][H][stride], then a
+// (max, sum) pair per (sequence, head, partition).
+struct WeightsPlan {
+    size_t scores_offset, ml_offset, bytes;
+    int64_t score_stride;
+};
+
+WeightsPlan plan_weights(const Plan& plan, int32_t num_seqs, int32_t num_heads, int32_t max_ctx) {
+    WeightsPlan w;
+    const size_t rows = (size_t)num_seqs * num_heads;
+    w.score_stride = round_up16(max_ctx > 16 ? max_ctx : 16);
+    w.scores_offset = (plan.ws_full + 255) / 256 * 256;
+    w.ml_offset = (w.scores_offset + rows * w.score_stride * sizeof(float) + 255) / 256 * 256;
+    w.bytes = w.ml_offset + rows * plan.num_partitions * 2 * sizeof(float);
+    return w;
+}
+
 }  // namespace
 
 int pa::report_error(int code, const char* fmt, ...) {
@@ -315,7 +353,8 @@ static int decode_impl(void* out, const void* q, const void* k_cache, const void
                        int32_t group_size, int32_t partition_size, void* workspace,
                        size_t workspace_bytes, void* stream, const int32_t* query_start = nullptr,
                        int32_t num_query_tokens = -1, int32_t max_query_len = 0,
-                       const float* k_scale = nullptr, const float* v_scale = nullptr) {
+                       const float* k_scale = nullptr, const float* v_scale = nullptr,
+                       float* weights = nullptr, int64_t weights_stride = 0) {
     Plan plan;
     if (cache && quantised(cache->dtype) != (k_scale != nullptr || v_scale != nullptr))
         return fail(PA_ERR_DTYPE, quantised(cache->dtype)
@@ -349,6 +388,20 @@ static int decode_impl(void* out, const void* q, const void* k_cache, const void
                     "block_size %d", max_context_len, block_table_stride, cache->block_size);
     if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "scale is not finite");
     const bool ws_aligned = (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0;
+    WeightsPlan wp;
+    if (weights) {
+        if ((reinterpret_cast<uintptr_t>(weights) & 3u) != 0)
+            return fail(PA_ERR_ALIGN, "pa_decode_weights: weights must be 4-byte aligned");
+        if (weights_stride < max_context_len)
+            return fail(PA_ERR_INVALID_ARG, "pa_decode_weights: weights_stride %lld below "
+                        "max_context_len %d", (long long)weights_stride, max_context_len);
+        wp = plan_weights(plan, num_seqs, num_heads, max_context_len);
+        if (!workspace || workspace_bytes < wp.bytes)
+            return fail(PA_ERR_WORKSPACE, "pa_decode_weights needs %zu workspace bytes, got %zu at %p",
+                        wp.bytes, workspace_bytes, workspace);
+        if (!ws_aligned)
+            return fail(PA_ERR_ALIGN, "pa_decode_weights: workspace must be 256-byte aligned");
+    }
     if (plan.ws_bytes > 0) {
         if (!workspace || workspace_bytes < plan.ws_bytes)
             return fail(PA_ERR_WORKSPACE, "pa_decode needs %zu workspace bytes, got %zu at %p",
@@ -396,6 +449,14 @@ static int decode_impl(void* out, const void* q, const void* k_cache, const void
     p.query_start = plan.multi ? query_start : nullptr;
     p.q_chunks = plan.q_chunks;
     p.num_rows = plan.multi ? num_query_tokens : num_seqs;
+    p.scores = nullptr;
+    p.score_stride = 0;
+    p.score_ml = nullptr;
+    if (weights) {
+        p.scores = reinterpret_cast<float*>(static_cast<char*>(workspace) + wp.scores_offset);
+        p.score_stride = wp.score_stride;
+        p.score_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + wp.ml_offset);
+    }
     p.sched = dyn_sched ? reinterpret_cast<unsigned int*>(static_cast<char*>(workspace) +
                                                           plan.sched_offset)
                         : nullptr;
@@ -421,6 +482,152 @@ static int decode_impl(void* out, const void* q, const void* k_cache, const void
         e = pa::launch_partition_reduce(p, cache->dtype, cache->head_dim, st);
         if (e != cudaSuccess) return fail_cuda(e, "pa_decode reduce launch");
     }
+    if (weights) {
+        pa::AddWeightsParams a;
+        a.scores = p.scores;
+        a.ml = p.score_ml;
+        a.context_lens = context_lens;
+        a.weights = weights;
+        a.score_stride = p.score_stride;
+        a.weights_stride = weights_stride;
+        a.max_context_len = max_context_len;
+        a.num_seqs = num_seqs;
+        a.num_heads = num_heads;
+        a.num_kv_heads = cache->num_kv_heads;
+        a.partition_size = plan.partition_size;
+        a.num_partitions = plan.num_partitions;
+        e = pa::launch_add_weights(a, st);
+        if (e != cudaSuccess) return fail_cuda(e, "pa_decode_weights launch");
+    }
+    return PA_OK;
+}
+
+// pa_rope_append / pa_rope_append_quant (k_scale, v_scale set).
+static int rope_impl(void* q_out, const void* q, const void* k, const void* v, int64_t q_stride,
+                     int64_t k_stride, int64_t v_stride, const int32_t* positions,
+                     const int64_t* slot_mapping, int32_t num_tokens, int32_t num_heads,
+                     void* k_cache, void* v_cache, const float* k_scale, const float* v_scale,
+                     const pa_cache_desc* cache, const pa_rope_desc* rope, void* stream) {
+    int rc = check_cache(cache);
+    if (rc != PA_OK) return rc;
+    if (!rope) return fail(PA_ERR_INVALID_ARG, "rotary descriptor is NULL");
+    if (rope->rotary_dim < 16 || rope->rotary_dim > cache->head_dim || rope->rotary_dim % 16 != 0)
+        return fail(PA_ERR_UNSUPPORTED, "rotary_dim %d must be a multiple of 16 in [16, head_dim %d]",
+                    rope->rotary_dim, cache->head_dim);
+    if (rope->pairs != PA_ROPE_HALF && rope->pairs != PA_ROPE_ADJACENT)
+        return fail(PA_ERR_INVALID_ARG, "pairs %d is not PA_ROPE_HALF or PA_ROPE_ADJACENT", rope->pairs);
+    if (rope->num_axes < 1 || rope->num_axes > PA_ROPE_MAX_AXES)
+        return fail(PA_ERR_INVALID_ARG, "num_axes %d outside [1, %d]", rope->num_axes, PA_ROPE_MAX_AXES);
+    if (!std::isfinite(rope->mscale)) return fail(PA_ERR_INVALID_ARG, "mscale is not finite");
+    const int half = rope->rotary_dim / 2;
+    pa::RopeParams p;
+    for (int i = 0; i < half; ++i) {
+        if (!std::isfinite(rope->inv_freq[i]))
+            return fail(PA_ERR_INVALID_ARG, "inv_freq[%d] is not finite", i);
+        if (rope->axis[i] >= rope->num_axes)
+            return fail(PA_ERR_INVALID_ARG, "axis[%d] = %d, num_axes %d", i, rope->axis[i], rope->num_axes);
+        // turns per position modulo 1, in units of 2^-64 (64-bit significand)
+        const long double t = (long double)rope->inv_freq[i] / 6.283185307179586476925286766559L;
+        p.turns[i] = (uint64_t)std::min(18446744073709551615.0L, std::floor((t - std::floor(t)) * 0x1p64L));
+        p.axis[i] = rope->axis[i];
+    }
+    if (num_heads < 0 || num_heads > 65535)
+        return fail(PA_ERR_INVALID_ARG, "num_heads %d outside [0, 65535]", num_heads);
+    if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens %d is negative", num_tokens);
+    if (num_tokens == 0) return PA_OK;
+    if ((num_heads > 0 && (!q_out || !q)) || !k || !v || !positions || !slot_mapping || !k_cache ||
+        !v_cache)
+        return fail(PA_ERR_INVALID_ARG, "pa_rope_append: NULL pointer argument");
+    if (!aligned16(q_out) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(k_cache) ||
+        !aligned16(v_cache))
+        return fail(PA_ERR_ALIGN, "pa_rope_append: q_out, q, k, v and the caches must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(positions) & 3u) != 0 ||
+        (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) != 0 ||
+        (reinterpret_cast<uintptr_t>(k_scale) & 3u) != 0 ||
+        (reinterpret_cast<uintptr_t>(v_scale) & 3u) != 0)
+        return fail(PA_ERR_ALIGN, "pa_rope_append: slot_mapping 8-byte, positions and scales 4-byte aligned");
+    const int64_t q_row = (int64_t)num_heads * cache->head_dim;
+    const int64_t kv_row = (int64_t)cache->num_kv_heads * cache->head_dim;
+    const int e = cache->dtype == PA_F32 ? 4 : 2;
+    if ((rc = check_stride("q", q_stride, q_row, e)) != PA_OK) return rc;
+    if ((rc = check_stride("k", k_stride, kv_row, e)) != PA_OK) return rc;
+    if ((rc = check_stride("v", v_stride, kv_row, e)) != PA_OK) return rc;
+    if (num_heads > 0) {
+        const size_t ob = (size_t)num_tokens * q_row * e;
+        if (overlap(q_out, ob, q, strided_bytes(num_tokens, q_stride, q_row, e)) ||
+            overlap(q_out, ob, k, strided_bytes(num_tokens, k_stride, kv_row, e)) ||
+            overlap(q_out, ob, v, strided_bytes(num_tokens, v_stride, kv_row, e)))
+            return fail(PA_ERR_INVALID_ARG, "pa_rope_append: q_out overlaps q, k or v");
+    }
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_out = q_out;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.positions = positions;
+    p.slot_mapping = slot_mapping;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.num_slots = (int64_t)cache->num_blocks * cache->block_size;
+    p.num_tokens = num_tokens;
+    p.num_heads = num_heads;
+    p.num_kv_heads = cache->num_kv_heads;
+    p.head_dim = cache->head_dim;
+    p.block_size = cache->block_size;
+    p.log2_block_size = ilog2_exact(cache->block_size);
+    p.half = half;
+    p.adjacent = rope->pairs == PA_ROPE_ADJACENT;
+    p.tokens_per_cta = 1;
+    p.mscale = rope->mscale;
+    cudaError_t ce = pa::launch_rope_append(p, cache->dtype, static_cast<cudaStream_t>(stream));
+    return ce == cudaSuccess ? PA_OK : fail_cuda(ce, "pa_rope_append launch");
+}
+
+// Checks and parameters shared by pa_prefill and pa_prefill_weights.
+static int prefill_params(pa::PrefillParams* p, const void* q, const void* k, int64_t q_stride,
+                          int64_t k_stride, const int32_t* cu_seqlens, int32_t num_seqs,
+                          int32_t total_tokens, int32_t max_seq_len, int32_t num_heads,
+                          int32_t num_kv_heads, int32_t head_dim, int32_t dtype, float scale) {
+    if (dtype != PA_F32 && dtype != PA_BF16)
+        return fail(PA_ERR_DTYPE, "prompt attention: dtype %d is not PA_F32 or PA_BF16", dtype);
+    if (head_dim != 64 && head_dim != 128)
+        return fail(PA_ERR_UNSUPPORTED, "head_dim %d not compiled (64 or 128)", head_dim);
+    if (num_kv_heads <= 0 || num_heads <= 0 || num_heads > 65535 || num_heads % num_kv_heads != 0)
+        return fail(PA_ERR_INVALID_ARG, "num_heads %d must be positive and a multiple of "
+                    "num_kv_heads %d", num_heads, num_kv_heads);
+    if (num_seqs < 0 || num_seqs > 65535)
+        return fail(PA_ERR_INVALID_ARG, "num_seqs %d outside [0, 65535]", num_seqs);
+    if (total_tokens < 0 || max_seq_len < 0)
+        return fail(PA_ERR_INVALID_ARG, "total_tokens %d or max_seq_len %d is negative", total_tokens,
+                    max_seq_len);
+    if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "scale is not finite");
+    const int e = dtype == PA_F32 ? 4 : 2;
+    int rc;
+    if ((rc = check_stride("q", q_stride, (int64_t)num_heads * head_dim, e)) != PA_OK) return rc;
+    if ((rc = check_stride("k", k_stride, (int64_t)num_kv_heads * head_dim, e)) != PA_OK) return rc;
+    p->out = nullptr;
+    p->q = q;
+    p->k = k;
+    p->v = nullptr;
+    p->cu_seqlens = cu_seqlens;
+    p->lse = nullptr;
+    p->weights = nullptr;
+    p->q_stride = q_stride;
+    p->k_stride = k_stride;
+    p->v_stride = 0;
+    p->weights_stride = 0;
+    p->num_seqs = num_seqs;
+    p->total_tokens = total_tokens;
+    p->max_seq_len = max_seq_len;
+    p->num_heads = num_heads;
+    p->num_kv_heads = num_kv_heads;
+    p->head_dim = head_dim;
+    p->last_queries = 0;
+    p->scale_log2 = scale * 1.4426950408889634f;
     return PA_OK;
 }
 
@@ -523,9 +730,6 @@ int pa_block_swap(const int64_t* src_dst_pairs, int32_t num_pairs, const void* s
     const size_t dbytes = block_bytes * (size_t)dst->num_blocks;
     const char* sv = static_cast<const char*>(src_v);
     const char* dv = static_cast<const char*>(dst_v);
-    auto overlap = [](const char* a, size_t na, const char* b, size_t nb) {
-        return a < b + nb && b < a + na;
-    };
     if (overlap(sk, sbytes, dk, dbytes) || overlap(sk, sbytes, dv, dbytes) ||
         overlap(sv, sbytes, dk, dbytes) || overlap(sv, sbytes, dv, dbytes) ||
         overlap(dk, dbytes, dv, dbytes))
@@ -687,6 +891,205 @@ int pa_set_grouped_consumer(int consumer) {
     return pa::set_grouped_consumer(consumer);
 }
 
+int pa_rope_append(void* q_out, const void* q, const void* k, const void* v, int64_t q_stride,
+                   int64_t k_stride, int64_t v_stride, const int32_t* positions,
+                   const int64_t* slot_mapping, int32_t num_tokens, int32_t num_heads,
+                   void* k_cache, void* v_cache, const pa_cache_desc* cache,
+                   const pa_rope_desc* rope, void* stream) {
+    if (cache && quantised(cache->dtype))
+        return fail(PA_ERR_DTYPE, "a quantised cache is written through pa_rope_append_quant");
+    return rope_impl(q_out, q, k, v, q_stride, k_stride, v_stride, positions, slot_mapping, num_tokens,
+                     num_heads, k_cache, v_cache, nullptr, nullptr, cache, rope, stream);
+}
+
+int pa_rope_append_quant(void* q_out, const void* q, const void* k, const void* v,
+                         int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                         const int32_t* positions, const int64_t* slot_mapping,
+                         int32_t num_tokens, int32_t num_heads, void* k_cache, void* v_cache,
+                         const float* k_scale, const float* v_scale, const pa_cache_desc* cache,
+                         const pa_rope_desc* rope, void* stream) {
+    if (cache && !quantised(cache->dtype))
+        return fail(PA_ERR_DTYPE, "pa_rope_append_quant needs a PA_FP8_E4M3 or PA_INT8 cache");
+    if (!k_scale || !v_scale)
+        return fail(PA_ERR_INVALID_ARG, "pa_rope_append_quant: k_scale and v_scale are required");
+    return rope_impl(q_out, q, k, v, q_stride, k_stride, v_stride, positions, slot_mapping, num_tokens,
+                     num_heads, k_cache, v_cache, k_scale, v_scale, cache, rope, stream);
+}
+
+int pa_prefill(void* out, const void* q, const void* k, const void* v, int64_t q_stride,
+               int64_t k_stride, int64_t v_stride, const int32_t* cu_seqlens, int32_t num_seqs,
+               int32_t total_tokens, int32_t max_seq_len, int32_t num_heads,
+               int32_t num_kv_heads, int32_t head_dim, int32_t dtype, float scale, float* lse,
+               void* stream) {
+    pa::PrefillParams p;
+    int rc = prefill_params(&p, q, k, q_stride, k_stride, cu_seqlens, num_seqs, total_tokens,
+                            max_seq_len, num_heads, num_kv_heads, head_dim, dtype, scale);
+    if (rc != PA_OK) return rc;
+    const int e = elem_bytes(dtype);
+    const int64_t q_row = (int64_t)num_heads * head_dim, kv_row = (int64_t)num_kv_heads * head_dim;
+    if ((rc = check_stride("v", v_stride, kv_row, e)) != PA_OK) return rc;
+    if (num_seqs == 0 || total_tokens == 0 || max_seq_len == 0) return PA_OK;
+    if (!out || !q || !k || !v || !cu_seqlens)
+        return fail(PA_ERR_INVALID_ARG, "pa_prefill: NULL pointer argument");
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k) || !aligned16(v))
+        return fail(PA_ERR_ALIGN, "pa_prefill: out, q, k and v must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) != 0 || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+        return fail(PA_ERR_ALIGN, "pa_prefill: cu_seqlens and lse must be 4-byte aligned");
+    const size_t ob = (size_t)total_tokens * q_row * e;
+    if (overlap(out, ob, q, strided_bytes(total_tokens, q_stride, q_row, e)) ||
+        overlap(out, ob, k, strided_bytes(total_tokens, k_stride, kv_row, e)) ||
+        overlap(out, ob, v, strided_bytes(total_tokens, v_stride, kv_row, e)))
+        return fail(PA_ERR_INVALID_ARG, "pa_prefill: out overlaps q, k or v");
+    p.out = out;
+    p.v = v;
+    p.v_stride = v_stride;
+    p.lse = lse;
+    cudaError_t ce = pa::launch_prefill(p, dtype, static_cast<cudaStream_t>(stream));
+    return ce == cudaSuccess ? PA_OK : fail_cuda(ce, "pa_prefill launch");
+}
+
+int pa_prefill_weights(float* weights, int64_t weights_stride, const void* q, const void* k,
+                       int64_t q_stride, int64_t k_stride, const float* lse,
+                       const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                       int32_t max_seq_len, int32_t num_heads, int32_t num_kv_heads,
+                       int32_t head_dim, int32_t dtype, float scale, int32_t last_queries,
+                       void* stream) {
+    pa::PrefillParams p;
+    int rc = prefill_params(&p, q, k, q_stride, k_stride, cu_seqlens, num_seqs, total_tokens,
+                            max_seq_len, num_heads, num_kv_heads, head_dim, dtype, scale);
+    if (rc != PA_OK) return rc;
+    if (last_queries < 0)
+        return fail(PA_ERR_INVALID_ARG, "last_queries %d is negative", last_queries);
+    if (weights_stride < max_seq_len)
+        return fail(PA_ERR_INVALID_ARG, "pa_prefill_weights: weights_stride %lld below max_seq_len %d",
+                    (long long)weights_stride, max_seq_len);
+    const size_t rows = (size_t)num_seqs * num_kv_heads;
+    if (rows == 0 || weights_stride == 0) return PA_OK;
+    if (!weights || (total_tokens > 0 && (!q || !k || !lse || !cu_seqlens)))
+        return fail(PA_ERR_INVALID_ARG, "pa_prefill_weights: NULL pointer argument");
+    if (!aligned16(q) || !aligned16(k))
+        return fail(PA_ERR_ALIGN, "pa_prefill_weights: q and k must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(weights) & 3u) != 0 || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0 ||
+        (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) != 0)
+        return fail(PA_ERR_ALIGN, "pa_prefill_weights: weights, lse and cu_seqlens must be 4-byte aligned");
+    p.lse = const_cast<float*>(lse);
+    p.weights = weights;
+    p.weights_stride = weights_stride;
+    p.last_queries = last_queries;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t ce = cudaMemsetAsync(weights, 0, rows * weights_stride * sizeof(float), st);
+    if (ce != cudaSuccess) return fail_cuda(ce, "pa_prefill_weights memset");
+    if (total_tokens == 0 || max_seq_len == 0) return PA_OK;
+    ce = pa::launch_prefill_weights(p, dtype, st);
+    return ce == cudaSuccess ? PA_OK : fail_cuda(ce, "pa_prefill_weights launch");
+}
+
+int pa_decode_weights(void* out, float* weights, int64_t weights_stride, const void* q,
+                      const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                      int32_t block_table_stride, const int32_t* context_lens,
+                      int32_t max_context_len, int32_t num_seqs, int32_t num_heads, float scale,
+                      const pa_cache_desc* cache, int32_t partition_size, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+    if (!weights) return fail(PA_ERR_INVALID_ARG, "pa_decode_weights: weights is NULL");
+    return decode_impl(out, q, k_cache, v_cache, block_tables, block_table_stride, context_lens,
+                       max_context_len, num_seqs, num_heads, scale, cache, 1, partition_size,
+                       workspace, workspace_bytes, stream, nullptr, -1, 0, nullptr, nullptr, weights,
+                       weights_stride);
+}
+
+int pa_decode_weights_quant(void* out, float* weights, int64_t weights_stride, const void* q,
+                            const void* k_cache, const void* v_cache, const float* k_scale,
+                            const float* v_scale, const int32_t* block_tables,
+                            int32_t block_table_stride, const int32_t* context_lens,
+                            int32_t max_context_len, int32_t num_seqs, int32_t num_heads,
+                            float scale, const pa_cache_desc* cache, int32_t partition_size,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+    if (!k_scale || !v_scale)
+        return fail(PA_ERR_INVALID_ARG, "pa_decode_weights_quant: k_scale and v_scale are required");
+    if (!weights) return fail(PA_ERR_INVALID_ARG, "pa_decode_weights_quant: weights is NULL");
+    return decode_impl(out, q, k_cache, v_cache, block_tables, block_table_stride, context_lens,
+                       max_context_len, num_seqs, num_heads, scale, cache, 1, partition_size,
+                       workspace, workspace_bytes, stream, nullptr, -1, 0, k_scale, v_scale, weights,
+                       weights_stride);
+}
+
+size_t pa_decode_weights_workspace_size(int32_t num_seqs, int32_t num_heads,
+                                        int32_t max_context_len, const pa_cache_desc* cache,
+                                        int32_t partition_size) {
+    Plan plan;
+    if (plan_decode(num_seqs, num_heads, max_context_len, cache, partition_size, &plan) != PA_OK)
+        return 0;
+    return plan_weights(plan, num_seqs, num_heads, max_context_len).bytes;
+}
+
+int pa_evict(void* k_cache, void* v_cache, const int32_t* block_tables,
+             int32_t block_table_stride, const int32_t* context_lens, int32_t max_context_len,
+             int32_t num_seqs, const float* weights, float* weights_out, int64_t weights_stride,
+             int32_t* new_context_lens, int32_t* kept, int32_t budget, int32_t recent,
+             const pa_cache_desc* cache, void* stream) {
+    int rc = check_cache(cache);
+    if (rc != PA_OK) return rc;
+    if (num_seqs < 0 || num_seqs > 65535)
+        return fail(PA_ERR_INVALID_ARG, "num_seqs %d outside [0, 65535]", num_seqs);
+    if (cache->num_kv_heads > 65535)
+        return fail(PA_ERR_INVALID_ARG, "num_kv_heads %d above 65535", cache->num_kv_heads);
+    if (budget < 1 || recent < 0 || recent > budget)
+        return fail(PA_ERR_INVALID_ARG, "budget %d must be positive and recent %d in [0, budget]",
+                    budget, recent);
+    if (max_context_len < 0)
+        return fail(PA_ERR_INVALID_ARG, "max_context_len %d is negative", max_context_len);
+    if (max_context_len > pa_evict_max_context())
+        return fail(PA_ERR_UNSUPPORTED, "max_context_len %d above pa_evict_max_context() = %d",
+                    max_context_len, pa_evict_max_context());
+    if (weights_stride < max_context_len || weights_stride < budget)
+        return fail(PA_ERR_INVALID_ARG, "weights_stride %lld below max_context_len %d or budget %d",
+                    (long long)weights_stride, max_context_len, budget);
+    if (block_table_stride < 0 ||
+        (int64_t)block_table_stride * cache->block_size < (int64_t)max_context_len)
+        return fail(PA_ERR_INVALID_ARG, "max_context_len %d exceeds block_table_stride %d * "
+                    "block_size %d", max_context_len, block_table_stride, cache->block_size);
+    if (num_seqs == 0) return PA_OK;
+    if (!k_cache || !v_cache || !block_tables || !context_lens || !weights || !weights_out ||
+        !new_context_lens || !kept)
+        return fail(PA_ERR_INVALID_ARG, "pa_evict: NULL pointer argument");
+    if (!aligned16(k_cache) || !aligned16(v_cache))
+        return fail(PA_ERR_ALIGN, "pa_evict: the caches must be 16-byte aligned");
+    const void* words[6] = {block_tables, context_lens, weights, weights_out, new_context_lens, kept};
+    for (const void* w : words)
+        if ((reinterpret_cast<uintptr_t>(w) & 3u) != 0)
+            return fail(PA_ERR_ALIGN, "pa_evict: tables, lengths, weights and kept must be 4-byte aligned");
+    const size_t rows = (size_t)num_seqs * cache->num_kv_heads;
+    const size_t wb = rows * weights_stride * 4;
+    if (overlap(context_lens, (size_t)num_seqs * 4, new_context_lens, (size_t)num_seqs * 4))
+        return fail(PA_ERR_INVALID_ARG, "pa_evict: new_context_lens overlaps context_lens");
+    if (weights != weights_out && overlap(weights, wb, weights_out, wb))
+        return fail(PA_ERR_INVALID_ARG, "pa_evict: weights_out overlaps weights without being it");
+    pa::EvictParams p;
+    p.k_cache = static_cast<uint4*>(k_cache);
+    p.v_cache = static_cast<uint4*>(v_cache);
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.weights = weights;
+    p.weights_out = weights_out;
+    p.new_context_lens = new_context_lens;
+    p.kept = kept;
+    p.table_stride = block_table_stride;
+    p.weights_stride = weights_stride;
+    p.max_context_len = max_context_len;
+    p.num_seqs = num_seqs;
+    p.num_kv_heads = cache->num_kv_heads;
+    p.num_blocks = cache->num_blocks;
+    p.block_size = cache->block_size;
+    p.log2_block_size = ilog2_exact(cache->block_size);
+    p.row_vecs = cache->head_dim * elem_bytes(cache->dtype) / 16;
+    p.budget = budget;
+    p.recent = recent;
+    cudaError_t e = pa::launch_evict(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : fail_cuda(e, "pa_evict launch");
+}
+
+int pa_evict_max_context(void) { return pa::evict_max_context(); }
+
 int pa_sync_check(void* stream) {
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail_cuda(e, "pa_sync_check: stream");
@@ -694,13 +1097,25 @@ int pa_sync_check(void* stream) {
     if ((e = pa::read_status_copy(&a, true)) != cudaSuccess ||
         (e = pa::read_status_tma(&b, true)) != cudaSuccess)
         return fail_cuda(e, "pa_sync_check: status word");
+    // the calls around decode: rotary append and eviction beside the copies, prompt
+    // attention beside decode
+    unsigned x = 0;
+    if ((e = pa::read_status_rope(&x, true)) != cudaSuccess)
+        return fail_cuda(e, "pa_sync_check: status word");
+    a |= x;
+    if ((e = pa::read_status_evict(&x, true)) != cudaSuccess)
+        return fail_cuda(e, "pa_sync_check: status word");
+    a |= x;
+    if ((e = pa::read_status_prefill_simt(&x, true)) != cudaSuccess)
+        return fail_cuda(e, "pa_sync_check: status word");
+    b |= x;
     if ((a | b) & pa::kStatusSmemAlign)
         return fail(PA_ERR_CUDA, "a decode kernel found its shared memory misaligned and did not run");
     if ((a | b) & pa::kStatusTimeout)
         return fail(PA_ERR_TIMEOUT, "a bounded pipeline wait gave up (bits copy=%u decode=%u)", a, b);
     if ((a | b) & pa::kStatusBadIndex)
-        return fail(PA_ERR_BAD_INDEX, "a kernel met a block id, slot or context length outside "
-                    "its bounds (bits copy=%u decode=%u)", a, b);
+        return fail(PA_ERR_BAD_INDEX, "a kernel met a block id, slot, context length or prompt "
+                    "outside its bounds (bits copy=%u decode=%u)", a, b);
     return PA_OK;
 }
 

@@ -85,17 +85,6 @@ block_copy_kernel(const int64_t* __restrict__ pairs, uint4* __restrict__ k_cache
 // y = x / scale[head] (binary32 division): FP8 E4M3 rounded to nearest even
 // and saturated to +-448, or int8 clamped to +-127 then rounded to nearest
 // even. The slot is checked as in kv_append_kernel.
-__device__ __forceinline__ uint32_t e4m3x2_code(float lo, float hi) {
-    uint32_t d;
-    asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n\tcvt.u32.u16 %0, t;\n\t}"
-        : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-
-__device__ __forceinline__ uint32_t int8_code(float y) {
-    return (uint32_t)(__float2int_rn(fminf(fmaxf(y, -127.f), 127.f)) & 0xff);
-}
-
 template <int FMT>
 __global__ void __launch_bounds__(kThreads)
 kv_append_quant_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,

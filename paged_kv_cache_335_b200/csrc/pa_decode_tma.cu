@@ -36,6 +36,7 @@
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pa_tma.cuh"
+#include "pa_umma.cuh"
 
 namespace pa {
 
@@ -342,7 +343,10 @@ template <typename T, int D>
 using SimtGeom = Geom<T, D, PA_SIMT_CONSUMER_WARPS,
                       is_code_type<T>() ? PA_SIMT_CODES_RING_BYTES : PA_SIMT_RING_BYTES>;
 
-template <typename T, int D>
+// kScores (pa_decode_weights): every score (log2 units) also goes to p.scores, and
+// each partition's running max and the sum of its unrounded weights (lx) to
+// p.score_ml; what is computed for out is the same bit for bit.
+template <typename T, int D, bool kScores>
 __global__ void __launch_bounds__(SimtGeom<T, D>::kThreads)
 decode_tma_simt_kernel(const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, const DecodeParams p) {
@@ -405,7 +409,7 @@ decode_tma_simt_kernel(const __grid_constant__ CUtensorMap kmap,
     }
     __syncthreads();
 
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f, lx = 0.f;
     float acc[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
@@ -489,7 +493,16 @@ decode_tma_simt_kernel(const __grid_constant__ CUtensorMap kmap,
                     __syncwarp();
                     if (lane == 0) mbar_arrive(ring.empty + 8 * st);
                 }
-                if (!valid) continue;
+                if (!valid) {
+                    if constexpr (kScores) {
+#pragma unroll
+                        for (int it = 0; it < IPP; ++it) {
+                            const int tok = tok0 + (pass + it) * RPL + rs;
+                            if (c == 0 && tok < t1) p.scores[out_row * p.score_stride + tok] = -INFINITY;
+                        }
+                    }
+                    continue;
+                }
                 float sc[IPP];
 #pragma unroll
                 for (int it = 0; it < IPP; ++it) {
@@ -516,6 +529,9 @@ decode_tma_simt_kernel(const __grid_constant__ CUtensorMap kmap,
                         dot += __shfl_xor_sync(0xffffffffu, dot, off);
                     const int tok = tok0 + (pass + it) * RPL + rs;
                     sc[it] = tok < t1 ? dot : -INFINITY;
+                    if constexpr (kScores) {
+                        if (c == 0 && tok < t1) p.scores[out_row * p.score_stride + tok] = dot;
+                    }
                 }
                 float mt = sc[0];
 #pragma unroll
@@ -528,6 +544,7 @@ decode_tma_simt_kernel(const __grid_constant__ CUtensorMap kmap,
                 if (m_new != m) {  // warp-uniform; a factor of exactly 1 changes no bit
                     const float alpha = kFastExp ? ex2_approx(m - m_new) : exp2f(m - m_new);
                     l *= alpha;
+                    if constexpr (kScores) lx *= alpha;
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) acc[j] *= alpha;
                 }
@@ -538,6 +555,7 @@ decode_tma_simt_kernel(const __grid_constant__ CUtensorMap kmap,
                     if constexpr (kMixed) {
                         const __half ph = __float2half_rn(pr);  // the weight the products use
                         l += __half2float(ph);
+                        if constexpr (kScores) lx += pr;
                         if (tok < t1) {  // slots past the context may hold anything, even NaN
                             uint32_t vh2[VEC / 2];
                             codes_to_f16x2<T, !kBiased>(vr[it], vh2);
@@ -548,6 +566,7 @@ decode_tma_simt_kernel(const __grid_constant__ CUtensorMap kmap,
                         }
                     } else {
                         l += pr;
+                        if constexpr (kScores) lx += pr;
                         if (tok < t1) {  // slots past the context may hold anything, even NaN
                             float vf[VEC];
                             if constexpr (kBiased) int8_widen_biased(vr[it], vf);
@@ -567,6 +586,7 @@ decode_tma_simt_kernel(const __grid_constant__ CUtensorMap kmap,
 #pragma unroll
         for (int off = CPR; off < 32; off <<= 1) {
             l += __shfl_xor_sync(0xffffffffu, l, off);
+            if constexpr (kScores) lx += __shfl_xor_sync(0xffffffffu, lx, off);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], off);
         }
@@ -576,6 +596,7 @@ decode_tma_simt_kernel(const __grid_constant__ CUtensorMap kmap,
     float* sm_o = reinterpret_cast<float*>(base);            // [warps][D]
     float* sm_m = sm_o + kConsumerWarps * D;                 // [warps]
     float* sm_l = sm_m + kConsumerWarps;
+    float* sm_lx = sm_l + kConsumerWarps;
     if (warp < kConsumerWarps) {
         const int c = lane % CPR, rs = lane / CPR;
         if (rs == 0) {
@@ -585,6 +606,7 @@ decode_tma_simt_kernel(const __grid_constant__ CUtensorMap kmap,
         if (lane == 0) {
             sm_m[warp] = m;
             sm_l[warp] = l;
+            if constexpr (kScores) sm_lx[warp] = lx;
         }
     }
     __syncthreads();
@@ -609,6 +631,16 @@ decode_tma_simt_kernel(const __grid_constant__ CUtensorMap kmap,
             Elem<TQ>::store(p.out, out_row * DQ + d, val);
         else
             p.ws_o[(out_row * p.num_partitions + part) * DQ + d] = val;
+    }
+    if constexpr (kScores) {
+        if (threadIdx.x == 0) {
+            float Lx = 0.f;
+#pragma unroll
+            for (int w = 0; w < kConsumerWarps; ++w) Lx = fmaf(sm_lx[w], wgt[w], Lx);
+            float* ml = p.score_ml + (out_row * p.num_partitions + part) * 2;
+            ml[0] = M;
+            ml[1] = Lx;
+        }
     }
     if (p.num_partitions > 1 && threadIdx.x == 0) {
         float* ml = p.ws_ml + (out_row * p.num_partitions + part) * 2;
@@ -698,15 +730,31 @@ __device__ __forceinline__ void mma_load_v(uint32_t vb, int r, int c, uint4 (&vr
     }
 }
 
+// Scores of tokens r (lo) and r + 8 (hi) of a sub-tile, for two heads.
+__device__ __forceinline__ void store_scores(float* so0, float* so1, int r, bool lo_ok, bool hi_ok,
+                                             float s0, float s1, float s2, float s3) {
+    if (so0 != nullptr) {
+        if (lo_ok) so0[r] = s0;
+        if (hi_ok) so0[r + 8] = s2;
+    }
+    if (so1 != nullptr) {
+        if (lo_ok) so1[r] = s1;
+        if (hi_ok) so1[r + 8] = s3;
+    }
+}
+
 // Online-softmax update with the sub-tile's scores and O^T += V^T . P^T.
 // nvalid = tokens of the sub-tile inside the context (>= 1). State: acc = O^T
 // fragments (rows head_dim 64*(t/4) + 8r + 2*(t%4) (+1), cols heads 2c, 2c+1),
 // m0/m1 running max (log2 units), l0/l1 this thread's share of the sums.
-template <int D>
+// kScores: the scores of heads 2c, 2c + 1 also go to so0[token], so1[token]
+// (nullptr: no such head), and lx0, lx1 sum the weights before their rounding.
+template <int D, bool kScores = false>
 __device__ __forceinline__ void mma_softmax_pv(const float (&sc)[4], uint4 (&vr)[4][D / 64],
                                                int nvalid, float scale_log2, int r, int c,
                                                float (&acc)[D / 16][4], float& m0, float& m1,
-                                               float& l0, float& l1) {
+                                               float& l0, float& l1, float* so0, float* so1,
+                                               float& lx0, float& lx1) {
     constexpr int VCH = D / 64;
     constexpr int MT = D / 16;
     const bool lo_ok = r < nvalid, hi_ok = r + 8 < nvalid;
@@ -714,6 +762,7 @@ __device__ __forceinline__ void mma_softmax_pv(const float (&sc)[4], uint4 (&vr)
     const float s1 = lo_ok ? sc[1] * scale_log2 : -INFINITY;  // token r,   head 2c+1
     const float s2 = hi_ok ? sc[2] * scale_log2 : -INFINITY;  // token r+8, head 2c
     const float s3 = hi_ok ? sc[3] * scale_log2 : -INFINITY;  // token r+8, head 2c+1
+    if constexpr (kScores) store_scores(so0, so1, r, lo_ok, hi_ok, s0, s1, s2, s3);
     float mx0 = fmaxf(s0, s2), mx1 = fmaxf(s1, s3);
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
@@ -726,11 +775,17 @@ __device__ __forceinline__ void mma_softmax_pv(const float (&sc)[4], uint4 (&vr)
     const bool moved = __any_sync(0xffffffffu, mn0 != m0 || mn1 != m1);
     const float al0 = moved ? exp2f(m0 - mn0) : 1.f;
     const float al1 = moved ? exp2f(m1 - mn1) : 1.f;
-    const uint32_t x0 = pack_bf16x2(exp2f(s0 - mn0), exp2f(s1 - mn1));
-    const uint32_t x1 = pack_bf16x2(exp2f(s2 - mn0), exp2f(s3 - mn1));
+    const float e0 = exp2f(s0 - mn0), e1 = exp2f(s1 - mn1);
+    const float e2 = exp2f(s2 - mn0), e3 = exp2f(s3 - mn1);
+    const uint32_t x0 = pack_bf16x2(e0, e1);
+    const uint32_t x1 = pack_bf16x2(e2, e3);
     // the sums use the same rounded weights the PV product sees
     l0 = fmaf(l0, al0, bf16_lo(x0) + bf16_lo(x1));
     l1 = fmaf(l1, al1, bf16_hi(x0) + bf16_hi(x1));
+    if constexpr (kScores) {
+        lx0 = fmaf(lx0, al0, e0 + e2);
+        lx1 = fmaf(lx1, al1, e1 + e3);
+    }
     m0 = mn0;
     m1 = mn1;
     if (moved) {
@@ -907,15 +962,17 @@ __device__ __forceinline__ void codes_load_v(uint32_t vb, int r, int c, uint4 (&
 
 // As mma_softmax_pv, over codes: scores scaled by scale_log2 x k_scale (sl),
 // weights packed as f16, V^T fragments built from the code chunks.
-template <typename TC>
+template <typename TC, bool kScores = false>
 __device__ __forceinline__ void codes_softmax_pv(const float (&sc)[4], uint4 (&vr)[4], int nvalid,
                                                  float sl, int r, int c, float (&acc)[8][4],
-                                                 float& m0, float& m1, float& l0, float& l1) {
+                                                 float& m0, float& m1, float& l0, float& l1,
+                                                 float* so0, float* so1, float& lx0, float& lx1) {
     const bool lo_ok = r < nvalid, hi_ok = r + 8 < nvalid;
     const float s0 = lo_ok ? sc[0] * sl : -INFINITY;
     const float s1 = lo_ok ? sc[1] * sl : -INFINITY;
     const float s2 = hi_ok ? sc[2] * sl : -INFINITY;
     const float s3 = hi_ok ? sc[3] * sl : -INFINITY;
+    if constexpr (kScores) store_scores(so0, so1, r, lo_ok, hi_ok, s0, s1, s2, s3);
     float mx0 = fmaxf(s0, s2), mx1 = fmaxf(s1, s3);
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
@@ -926,10 +983,16 @@ __device__ __forceinline__ void codes_softmax_pv(const float (&sc)[4], uint4 (&v
     const bool moved = __any_sync(0xffffffffu, mn0 != m0 || mn1 != m1);
     const float al0 = moved ? exp2f(m0 - mn0) : 1.f;
     const float al1 = moved ? exp2f(m1 - mn1) : 1.f;
-    const uint32_t x0 = pack_f16x2(exp2f(s0 - mn0), exp2f(s1 - mn1));
-    const uint32_t x1 = pack_f16x2(exp2f(s2 - mn0), exp2f(s3 - mn1));
+    const float e0 = exp2f(s0 - mn0), e1 = exp2f(s1 - mn1);
+    const float e2 = exp2f(s2 - mn0), e3 = exp2f(s3 - mn1);
+    const uint32_t x0 = pack_f16x2(e0, e1);
+    const uint32_t x1 = pack_f16x2(e2, e3);
     l0 = fmaf(l0, al0, f16_lo(x0) + f16_lo(x1));
     l1 = fmaf(l1, al1, f16_hi(x0) + f16_hi(x1));
+    if constexpr (kScores) {
+        lx0 = fmaf(lx0, al0, e0 + e2);
+        lx1 = fmaf(lx1, al1, e1 + e3);
+    }
     m0 = mn0;
     m1 = mn1;
     if (moved) {
@@ -1213,7 +1276,9 @@ __device__ __forceinline__ bool consumers_all(bool pred, int threads) {
 // entries fetched one 32-sub-tile batch ahead), while the consumers finish one
 // item (cross-warp merge, store) and start the next (q fragments fetched one
 // item ahead).
-template <int D, typename TC = __nv_bfloat16>
+// kScores (pa_decode_weights): see mma_softmax_pv; each partition's (max, lx)
+// goes to p.score_ml.
+template <int D, typename TC = __nv_bfloat16, bool kScores = false>
 __global__ void __launch_bounds__(MmaGeom<D, TC>::kThreads, PA_MMA_MIN_BLOCKS)
 decode_tma_mma_kernel(const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const DecodeParams p,
@@ -1223,11 +1288,13 @@ decode_tma_mma_kernel(const __grid_constant__ CUtensorMap kmap,
     constexpr bool kCodes = !std::is_same<TC, __nv_bfloat16>::value;
     static_assert(!kCodes || D == 128, "quantised codes: head_dim 128");
     static_assert(!kCodes || G::kCW <= 2, "the code consumer's head_dim order needs the register merge");
+    static_assert(!kScores || G::kCW <= 2, "the scores' (max, sum) pairs are stored by the register merge");
     constexpr int kConsumerWarps = G::kCW;
     constexpr int KCH = D / 32;  // 16-byte K chunks per row per thread (2 k-steps each)
     constexpr int VCH = D / 64;  // V boxes
     constexpr int MT = D / 16;   // PV m-tiles
     constexpr int OS = D + 1;    // merge-buffer row stride (floats)
+    constexpr int kMerge = merge_bytes<D>() + (kScores ? 2 * 32 * 4 : 0);  // + lx0, lx1
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     asm volatile("griddepcontrol.launch_dependents;");
 
@@ -1235,7 +1302,7 @@ decode_tma_mma_kernel(const __grid_constant__ CUtensorMap kmap,
     const int P = p.num_partitions;
     const int group = p.num_heads / p.num_kv_heads;
     Ring ring;
-    uint8_t* base = setup_ring<G>(smem_raw, ring, merge_bytes<D>() + kItemQBytes);
+    uint8_t* base = setup_ring<G>(smem_raw, ring, kMerge + kItemQBytes);
     if (base == nullptr) {
         if (threadIdx.x == 0) atomicOr(&s_status_tma, kStatusSmemAlign);
         return;
@@ -1243,7 +1310,7 @@ decode_tma_mma_kernel(const __grid_constant__ CUtensorMap kmap,
     float* merge_buf = reinterpret_cast<float*>(base + G::kRingBytes);
     int merge_sel = 0;  // which half of the double-buffered merge area this item uses
     const bool dyn = p.sched != nullptr;  // dynamic schedule (else item u to CTA u mod grid)
-    const ItemQueue iq = item_queue_setup(base + G::kRingBytes + merge_bytes<D>(), kConsumerWarps);
+    const ItemQueue iq = item_queue_setup(base + G::kRingBytes + kMerge, kConsumerWarps);
     ItemWalk walk;
     walk.k = 0;
     walk.kbase = 0;
@@ -1380,7 +1447,7 @@ decode_tma_mma_kernel(const __grid_constant__ CUtensorMap kmap,
             float acc[MT][4];
 #pragma unroll
             for (int t = 0; t < MT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
-            float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+            float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, lx0 = 0.f, lx1 = 0.f;
 
             for (int i = warp; i < n_sub && !dead; i += kConsumerWarps) {
                 const int gi = g + i;
@@ -1396,6 +1463,17 @@ decode_tma_mma_kernel(const __grid_constant__ CUtensorMap kmap,
                 const uint32_t kb = ring.stages + st * G::kStageBytes;
                 const uint32_t vb = kb + G::kBoxes * kBoxBytes;
                 float sc[4];
+                float *so0 = nullptr, *so1 = nullptr;
+                if constexpr (kScores) {
+                    float* so = p.scores + (head0 + 2 * c) * p.score_stride + t0 + (i << 4);
+                    if (2 * c < group) so0 = so;
+                    if (2 * c + 1 < group) so1 = so + p.score_stride;
+                    if (!valid) {  // a block id outside the pool: nothing attended
+                        const int nv = t1 - (t0 + (i << 4));
+                        store_scores(so0, so1, r, r < nv, r + 8 < nv, -INFINITY, -INFINITY,
+                                     -INFINITY, -INFINITY);
+                    }
+                }
                 if constexpr (kCodes) {
                     codes_qk<TC>(kb, qcur, r, c, sc);
                     if constexpr (std::is_same<TC, Int8Code>::value) {
@@ -1409,7 +1487,8 @@ decode_tma_mma_kernel(const __grid_constant__ CUtensorMap kmap,
                     __syncwarp();
                     if (lane == 0) mbar_arrive(ring.empty + 8 * st);  // stage released
                     if (!valid) continue;
-                    codes_softmax_pv<TC>(sc, vr, t1 - (t0 + (i << 4)), sl, r, c, acc, m0, m1, l0, l1);
+                    codes_softmax_pv<TC, kScores>(sc, vr, t1 - (t0 + (i << 4)), sl, r, c, acc, m0, m1, l0,
+                                                  l1, so0, so1, lx0, lx1);
                 } else {
                     mma_qk<D>(kb, qcur, r, c, sc);
                     uint4 vr[4][VCH];
@@ -1417,7 +1496,8 @@ decode_tma_mma_kernel(const __grid_constant__ CUtensorMap kmap,
                     __syncwarp();
                     if (lane == 0) mbar_arrive(ring.empty + 8 * st);  // stage released
                     if (!valid) continue;
-                    mma_softmax_pv<D>(sc, vr, t1 - (t0 + (i << 4)), sl, r, c, acc, m0, m1, l0, l1);
+                    mma_softmax_pv<D, kScores>(sc, vr, t1 - (t0 + (i << 4)), sl, r, c, acc, m0, m1, l0, l1,
+                                               so0, so1, lx0, lx1);
                 }
             }
             g += n_sub;
@@ -1431,6 +1511,10 @@ decode_tma_mma_kernel(const __grid_constant__ CUtensorMap kmap,
             for (int off = 4; off < 32; off <<= 1) {
                 l0 += __shfl_xor_sync(0xffffffffu, l0, off);
                 l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+                if constexpr (kScores) {
+                    lx0 += __shfl_xor_sync(0xffffffffu, lx0, off);
+                    lx1 += __shfl_xor_sync(0xffffffffu, lx1, off);
+                }
             }
             if constexpr (kConsumerWarps == 2) {
                 // Warp 1 hands its state to warp 0 in register order (conflict-free);
@@ -1445,6 +1529,10 @@ decode_tma_mma_kernel(const __grid_constant__ CUtensorMap kmap,
                     xb[(MT * 4 + 1) * 32 + lane] = m1;
                     xb[(MT * 4 + 2) * 32 + lane] = l0;
                     xb[(MT * 4 + 3) * 32 + lane] = l1;
+                    if constexpr (kScores) {
+                        xb[(MT * 4 + 4) * 32 + lane] = lx0;
+                        xb[(MT * 4 + 5) * 32 + lane] = lx1;
+                    }
                 }
                 named_barrier(1, 64);
                 if (warp == 0) {
@@ -1464,8 +1552,25 @@ decode_tma_mma_kernel(const __grid_constant__ CUtensorMap kmap,
                     }
                     l0 = fmaf(lb0, wb0, l0 * wa0);
                     l1 = fmaf(lb1, wb1, l1 * wa1);
+                    if constexpr (kScores) {
+                        lx0 = fmaf(xb[(MT * 4 + 4) * 32 + lane], wb0, lx0 * wa0);
+                        lx1 = fmaf(xb[(MT * 4 + 5) * 32 + lane], wb1, lx1 * wa1);
+                    }
                     m0 = M0;
                     m1 = M1;
+                }
+            }
+            if constexpr (kScores) {
+                if (warp == 0 && r == 0) {
+                    float* ml = p.score_ml + ((head0 + 2 * c) * P + cur.part) * 2;
+                    if (2 * c < group) {
+                        ml[0] = m0;
+                        ml[1] = lx0;
+                    }
+                    if (2 * c + 1 < group) {
+                        ml[2 * P] = m1;
+                        ml[2 * P + 1] = lx1;
+                    }
                 }
             }
             if constexpr (kConsumerWarps <= 2) {
@@ -2644,87 +2749,6 @@ decode_tma_grouped_kernel(const __grid_constant__ CUtensorMap kmap,
 }
 
 // ---------------------------------------------------------------------------
-// 5th-generation tensor-core (tcgen05) helpers.
-// ---------------------------------------------------------------------------
-// Shared-memory matrix descriptor: start address, leading / stride byte
-// offsets (16-byte units), descriptor version 1, layout 2 = 128-byte swizzle.
-__device__ __forceinline__ uint64_t umma_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
-}
-// Instruction descriptor for kind::f16: fp32 accumulator, bf16 (or, with
-// f16, f16) A and B, A K-major, B K-major or MN-major, shape M x N.
-__host__ __device__ constexpr uint32_t umma_idesc(int m, int n, bool b_mn_major, bool f16 = false,
-                                                  bool a_mn_major = false) {
-    return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) |
-           ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
-           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
-}
-// D (TMEM) (+)= A (shared) . B (shared)^T, issued by one thread.
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                        bool acc) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
-}
-// D (TMEM) (+)= A (TMEM) . B (shared)^T.
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                        bool acc) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 :: "r"(d), "r"(a_tmem), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
-}
-// The mbarrier at `bar` gets one arrival once every tcgen05 operation this
-// thread issued so far has completed.
-__device__ __forceinline__ void umma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                 :: "r"(bar) : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-// generic-proxy shared-memory writes made visible to the tensor core's reads
-__device__ __forceinline__ void fence_async_smem() {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                 :: "r"(slot), "r"(ncols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
-                 :: "r"(taddr), "r"(ncols) : "memory");
-}
-// Loads / stores of this warp's 32 TMEM lanes (32x32b): thread t reads or
-// writes lane (lane of taddr) + t, consecutive 32-bit columns.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-                 : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-                 : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                 :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
-                 :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]) : "memory");
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// ---------------------------------------------------------------------------
 // Grouped and multi-token decode on the 5th-generation tensor cores (head_dim
 // 128, at most 32 query columns (member, head) per item; bf16 caches, or
 // FP8 E4M3 / int8 codes converted to f16 in shared memory).
@@ -3442,29 +3466,36 @@ decode_umma_grouped_kernel(const __grid_constant__ CUtensorMap kmap,
     if (lane == 0) mbar_arrive(B.done);
 }
 
-template <typename T, int D>
-cudaError_t launch_simt_t(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm,
+template <typename T, int D, bool kScores>
+cudaError_t launch_simt_k(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm,
                           cudaStream_t stream) {
     using G = SimtGeom<T, D>;
     constexpr size_t smem = smem_bytes<G>();
-    cudaError_t e = cudaFuncSetAttribute(decode_tma_simt_kernel<T, D>,
+    cudaError_t e = cudaFuncSetAttribute(decode_tma_simt_kernel<T, D, kScores>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(decode_tma_simt_kernel<T, D>,
+    e = cudaFuncSetAttribute(decode_tma_simt_kernel<T, D, kScores>,
                              cudaFuncAttributePreferredSharedMemoryCarveout,
                              (int)cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     dim3 grid((unsigned)p.num_partitions, (unsigned)p.num_heads, (unsigned)p.num_rows);
-    decode_tma_simt_kernel<T, D><<<grid, G::kThreads, smem, stream>>>(km, vm, p);
+    decode_tma_simt_kernel<T, D, kScores><<<grid, G::kThreads, smem, stream>>>(km, vm, p);
     return cudaGetLastError();
 }
 
-template <int D, typename TC = __nv_bfloat16>
-cudaError_t launch_mma_t(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm,
+template <typename T, int D>
+cudaError_t launch_simt_t(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm,
+                          cudaStream_t stream) {
+    return p.scores != nullptr ? launch_simt_k<T, D, true>(p, km, vm, stream)
+                               : launch_simt_k<T, D, false>(p, km, vm, stream);
+}
+
+template <int D, typename TC, bool kScores>
+cudaError_t launch_mma_k(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm,
                          cudaStream_t stream) {
     using G = MmaGeom<D, TC>;
-    constexpr size_t smem = smem_bytes<G>(merge_bytes<D>() + kItemQBytes);
-    auto kernel = decode_tma_mma_kernel<D, TC>;
+    constexpr size_t smem = smem_bytes<G>(merge_bytes<D>() + (kScores ? 2 * 32 * 4 : 0) + kItemQBytes);
+    auto kernel = decode_tma_mma_kernel<D, TC, kScores>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
@@ -3488,6 +3519,13 @@ cudaError_t launch_mma_t(const DecodeParams& p, const CUtensorMap& km, const CUt
     const unsigned grid = (unsigned)(items < slots ? items : slots);
     kernel<<<grid, G::kThreads, smem, stream>>>(km, vm, p, (int)items);
     return cudaGetLastError();
+}
+
+template <int D, typename TC = __nv_bfloat16>
+cudaError_t launch_mma_t(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm,
+                         cudaStream_t stream) {
+    return p.scores != nullptr ? launch_mma_k<D, TC, true>(p, km, vm, stream)
+                               : launch_mma_k<D, TC, false>(p, km, vm, stream);
 }
 
 template <typename TC>

@@ -142,6 +142,20 @@ __device__ __forceinline__ void int8_widen_biased(const uint4& c, float (&f)[16]
     }
 }
 
+// Codes of the quantising appends: two E4M3 codes (first value in the low byte;
+// round to nearest even, saturating), or one int8 code (clamped, then rounded to
+// nearest even).
+__device__ __forceinline__ uint32_t e4m3x2_code(float lo, float hi) {
+    uint32_t d;
+    asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n\tcvt.u32.u16 %0, t;\n\t}"
+        : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t int8_code(float y) {
+    return (uint32_t)(__float2int_rn(fminf(fmaxf(y, -127.f), 127.f)) & 0xff);
+}
+
 // q / out element type for a cache element type (quantised caches: bf16).
 template <typename TC> struct QType { using type = TC; };
 template <> struct QType<E4M3Code> { using type = __nv_bfloat16; };

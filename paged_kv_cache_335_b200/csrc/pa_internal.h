@@ -58,6 +58,81 @@ struct DecodeParams {
     // the launch, from which CTAs claim work items in order (nullptr: static
     // schedule, item u to CTA u mod grid).
     unsigned int* sched;
+    // pa_decode_weights, else nullptr: scores [row of out][score_stride] (log2 units;
+    // a token's at its position) and per (row, partition) the pair (running max,
+    // sum of the unrounded weights).
+    float* scores;
+    int64_t score_stride;
+    float* score_ml;
+};
+
+// One launch of the rotary append (pa_rope.cu). Strides are in elements.
+struct RopeParams {
+    const void* q;              // [T] rows of num_heads x head_dim, q_stride apart
+    const void* k;
+    const void* v;
+    void* q_out;                // [T][num_heads][head_dim]
+    void* k_cache;
+    void* v_cache;
+    const int32_t* positions;   // [axes][T]
+    const int64_t* slot_mapping;
+    const float* k_scale;       // codes: [num_kv_heads]
+    const float* v_scale;
+    int64_t q_stride, k_stride, v_stride;
+    int64_t num_slots;
+    int32_t num_tokens, num_heads, num_kv_heads, head_dim;
+    int32_t block_size, log2_block_size;
+    int32_t half;               // rotary_dim / 2: frequencies
+    int32_t adjacent;           // pairs (2i, 2i + 1) instead of (i, i + half)
+    int32_t tokens_per_cta;
+    float mscale;
+    uint8_t axis[64];
+    uint64_t turns[64];         // inv_freq / (2 pi) mod 1, in units of 2^-64
+};
+
+// Eviction (pa_evict.cu).
+struct EvictParams {
+    uint4* k_cache;
+    uint4* v_cache;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const float* weights;       // [S][Hkv][weights_stride]
+    float* weights_out;
+    int32_t* new_context_lens;
+    int32_t* kept;              // [S][Hkv][budget]
+    int64_t table_stride;
+    int64_t weights_stride;
+    int32_t max_context_len, num_seqs, num_kv_heads, num_blocks;
+    int32_t block_size, log2_block_size, row_vecs;
+    int32_t budget, recent;
+};
+
+// weights += the softmax weights of a decode step (pa_evict.cu).
+struct AddWeightsParams {
+    const float* scores;        // [S][H][score_stride], log2 units
+    const float* ml;            // [S][H][P][2]
+    const int32_t* context_lens;
+    float* weights;             // [S][Hkv][weights_stride]
+    int64_t score_stride, weights_stride;
+    int32_t max_context_len, num_seqs, num_heads, num_kv_heads;
+    int32_t partition_size, num_partitions;
+};
+
+// Attention over whole packed prompts and the weights their tokens received
+// (pa_prefill_simt.cu). Strides in elements, between tokens.
+struct PrefillParams {
+    void* out;                  // [T][H][D]
+    const void* q;
+    const void* k;
+    const void* v;
+    const int32_t* cu_seqlens;  // [S + 1]
+    float* lse;                 // [H][T], natural log (pa_prefill_weights: read)
+    float* weights;             // [S][Hkv][weights_stride]
+    int64_t q_stride, k_stride, v_stride;
+    int64_t weights_stride;
+    int32_t num_seqs, total_tokens, max_seq_len, num_heads, num_kv_heads, head_dim;
+    int32_t last_queries;       // pa_prefill_weights: 0 = every query
+    float scale_log2;           // softmax scale * log2(e)
 };
 
 struct CopyParams {
@@ -121,6 +196,17 @@ cudaError_t launch_decode_grouped(const DecodeParams& p, int dtype, int head_dim
 cudaError_t launch_partition_reduce(const DecodeParams& p, int dtype, int head_dim,
                                     cudaStream_t stream);
 
+cudaError_t launch_rope_append(RopeParams p, int dtype, cudaStream_t stream);
+
+// Longest context pa_evict takes (its selection keeps two words per 32 tokens in
+// shared memory).
+int evict_max_context();
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
+cudaError_t launch_add_weights(const AddWeightsParams& p, cudaStream_t stream);
+
+cudaError_t launch_prefill(const PrefillParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_prefill_weights(const PrefillParams& p, int dtype, cudaStream_t stream);
+
 // Record `fmt` as this host thread's last error (read by pa_get_last_error)
 // and return `code`.
 int report_error(int code, const char* fmt, ...);
@@ -129,5 +215,8 @@ int report_error(int code, const char* fmt, ...);
 // last clear. Return cudaSuccess or the copy error.
 cudaError_t read_status_copy(unsigned* bits, bool clear);
 cudaError_t read_status_tma(unsigned* bits, bool clear);
+cudaError_t read_status_rope(unsigned* bits, bool clear);
+cudaError_t read_status_evict(unsigned* bits, bool clear);
+cudaError_t read_status_prefill_simt(unsigned* bits, bool clear);
 
 }  // namespace pa

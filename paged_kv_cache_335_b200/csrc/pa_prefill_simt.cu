@@ -1,0 +1,294 @@
+// pa_prefill_simt.cu — prompt attention and prompt weights on the CUDA cores, with
+// fp32 arithmetic.
+//
+// out[i] = softmax over t <= i of (scale q_i . k_t) applied to v, per prompt and head
+// ("PagedAttention原理详解…", § 显存消耗的三大来源, for every query of the prompt at
+// once), in one pass over the keys with the running maximum and sum of the
+// softmax (Milakov and Gimelshein, "Online normalizer calculation for softmax").
+//
+// CTA = 64 queries of one head against tiles of 64 keys; thread (ty, tx) of
+// 16 x 16 holds a 4 x 4 block of scores and a 4 x D/16 block of the output.
+// Q and K lie transposed in shared memory so that a thread reads its four
+// queries and four keys of one dimension as two 16-byte words per 16 fma. Bound
+// by the fp32 fma rate and the shared-memory reads that feed it.
+#include <math.h>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+#include "pa_prefill_tile.cuh"
+
+namespace pa {
+
+static __device__ unsigned int s_status_prefill_simt;
+
+namespace {
+
+constexpr int kB = 64;            // queries and keys of a tile
+constexpr int kThreads = 256;
+constexpr int kPad = kB + 4;      // row of a transposed tile (floats)
+
+// Four consecutive elements, widened.
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2((uint32_t)float_to_bf16_bits(v.x) | ((uint32_t)float_to_bf16_bits(v.y) << 16),
+                   (uint32_t)float_to_bf16_bits(v.z) | ((uint32_t)float_to_bf16_bits(v.w) << 16));
+}
+
+// Rows [row0, row0 + 64) x D of a packed tensor, transposed to dst[d][row];
+// rows at or past `end` become zeros.
+template <int D, typename T>
+__device__ __forceinline__ void load_t(float* dst, const T* src, int64_t stride, int row0, int end) {
+    for (int i = threadIdx.x; i < kB * (D / 4); i += kThreads) {
+        const int r = i % kB, c = i / kB;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row0 + r < end) v = load4(src + (int64_t)(row0 + r) * stride + 4 * c);
+        dst[(4 * c + 0) * kPad + r] = v.x;
+        dst[(4 * c + 1) * kPad + r] = v.y;
+        dst[(4 * c + 2) * kPad + r] = v.z;
+        dst[(4 * c + 3) * kPad + r] = v.w;
+    }
+}
+
+// s[4][4] = a . b for rows 4 ty .. of `at` and 4 tx .. of `bt` (both transposed).
+template <int D>
+__device__ __forceinline__ void dot_tile(const float* at, const float* bt, int ty, int tx, float (&s)[4][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 8
+    for (int d = 0; d < D; ++d) {
+        const float4 a = *reinterpret_cast<const float4*>(at + d * kPad + 4 * ty);
+        const float4 b = *reinterpret_cast<const float4*>(bt + d * kPad + 4 * tx);
+        const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = fmaf(av[i], bv[j], s[i][j]);
+    }
+}
+
+template <int D>
+constexpr size_t smem_prefill() {
+    return sizeof(float) * (2 * (size_t)D * kPad + (size_t)kB * D);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+prefill_simt_kernel(const PrefillParams p) {
+    extern __shared__ __align__(16) float sm[];
+    float* qt = sm;                  // [D][kPad]
+    float* kt = qt + D * kPad;       // [D][kPad]; then the weights [key][kPad]
+    float* vs = kt + D * kPad;       // [kB][D]
+    bool bad = false;
+    const PromptTile t = prompt_tile(p, kB, blockIdx.x, true, &bad);
+    const int h = blockIdx.y;
+    if (bad && blockIdx.x == 0 && h == 0) atomicOr(&s_status_prefill_simt, kStatusBadIndex);
+    if (t.seq < 0) return;
+    const int kh = h / (p.num_heads / p.num_kv_heads);
+    const T* q = static_cast<const T*>(p.q) + (int64_t)h * D;
+    const T* k = static_cast<const T*>(p.k) + (int64_t)kh * D;
+    const T* v = static_cast<const T*>(p.v) + (int64_t)kh * D;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int end = t.start + t.len, q0 = t.tile * kB;
+    load_t<D, T>(qt, q, p.q_stride, t.start + q0, end);
+    float o[4][D / 16], m[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) o[i][j] = 0.f;
+    }
+    for (int j0 = 0; j0 <= q0; j0 += kB) {
+        __syncthreads();
+        load_t<D, T>(kt, k, p.k_stride, t.start + j0, end);
+        for (int i = threadIdx.x; i < kB * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), c = i % (D / 4);
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (t.start + j0 + r < end)
+                x = load4(v + (int64_t)(t.start + j0 + r) * p.v_stride + 4 * c);
+            *reinterpret_cast<float4*>(vs + r * D + 4 * c) = x;
+        }
+        __syncthreads();
+        float s[4][4];
+        dot_tile<D>(qt, kt, ty, tx, s);
+        const bool diag = j0 == q0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = diag && 4 * tx + j > 4 * ty + i ? -INFINITY : s[i][j] * p.scale_log2;
+                mx = fmaxf(mx, s[i][j]);
+            }
+#pragma unroll
+            for (int off = 1; off < 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const float mn = fmaxf(m[i], mx);
+            const float al = exp2f(m[i] - mn);
+            m[i] = mn;
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = exp2f(s[i][j] - mn);
+                sum += s[i][j];
+            }
+            l[i] = fmaf(l[i], al, sum);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) o[i][j] *= al;
+        }
+        __syncthreads();  // the keys are no longer needed
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<float4*>(kt + (4 * tx + j) * kPad + 4 * ty) =
+                make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
+        __syncthreads();
+        // on the diagonal a key past the query is left out, not multiplied by a
+        // weight of 0: its value may be infinite or NaN
+#pragma unroll 4
+        for (int c = 0; c < kB; ++c) {
+            const float4 w4 = *reinterpret_cast<const float4*>(kt + c * kPad + 4 * ty);
+            const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+            for (int g = 0; g < D / 64; ++g) {
+                const float4 x4 = *reinterpret_cast<const float4*>(vs + c * D + 64 * g + 4 * tx);
+                const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (!diag || c <= 4 * ty + i) o[i][4 * g + j] = fmaf(w[i], x[j], o[i][4 * g + j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int off = 1; off < 16; off <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
+        const int row = q0 + 4 * ty + i;
+        if (row >= t.len) continue;
+        const float inv = 1.f / l[i];
+        T* dst = static_cast<T*>(p.out) + ((int64_t)(t.start + row) * p.num_heads + h) * D;
+#pragma unroll
+        for (int g = 0; g < D / 64; ++g)
+            store4(dst + 64 * g + 4 * tx, make_float4(o[i][4 * g] * inv, o[i][4 * g + 1] * inv,
+                                                      o[i][4 * g + 2] * inv, o[i][4 * g + 3] * inv));
+        if (p.lse != nullptr && tx == 0)
+            p.lse[(int64_t)h * p.total_tokens + t.start + row] = (m[i] + log2f(l[i])) * 0.6931471805599453f;
+    }
+}
+
+// weights[s][kh][t] = sum over the heads of the group and the queries i >= t of
+// exp(scale q_i . k_t - lse_i): CTA = 64 keys of one kv head against tiles of 64
+// queries. Every sum is formed in a fixed order.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+prefill_weights_simt_kernel(const PrefillParams p) {
+    extern __shared__ __align__(16) float sm[];
+    float* kt = sm;                  // [D][kPad]
+    float* qt = kt + D * kPad;
+    float* lq = qt + D * kPad;       // [kB] log-sum-exp of the queries, log2 units
+    bool bad = false;
+    const PromptTile t = prompt_tile(p, kB, blockIdx.x, false, &bad);
+    const int kh = blockIdx.y;
+    if (bad && blockIdx.x == 0 && kh == 0) atomicOr(&s_status_prefill_simt, kStatusBadIndex);
+    if (t.seq < 0) return;
+    const int group = p.num_heads / p.num_kv_heads;
+    const T* k = static_cast<const T*>(p.k) + (int64_t)kh * D;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int end = t.start + t.len, k0 = t.tile * kB;
+    const int first = p.last_queries > 0 ? max(0, t.len - p.last_queries) : 0;
+    load_t<D, T>(kt, k, p.k_stride, t.start + k0, end);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int g = 0; g < group; ++g) {
+        const int h = kh * group + g;
+        const T* q = static_cast<const T*>(p.q) + (int64_t)h * D;
+        for (int i0 = max(k0, first / kB * kB); i0 < t.len; i0 += kB) {
+            __syncthreads();
+            load_t<D, T>(qt, q, p.q_stride, t.start + i0, end);
+            if (threadIdx.x < kB) {
+                const int i = i0 + threadIdx.x;
+                lq[threadIdx.x] = i < t.len ? __ldg(p.lse + (int64_t)h * p.total_tokens + t.start + i) *
+                                                  1.4426950408889634f
+                                            : 0.f;
+            }
+            __syncthreads();
+            float s[4][4];
+            dot_tile<D>(kt, qt, ty, tx, s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int qi = i0 + 4 * tx + j;
+                    if (qi >= first && qi < t.len && k0 + 4 * ty + i <= qi)
+                        sum += exp2f(fmaf(s[i][j], p.scale_log2, -lq[4 * tx + j]));
+                }
+                acc[i] += sum;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int off = 1; off < 16; off <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
+        const int tok = k0 + 4 * ty + i;
+        if (tx == 0 && tok < t.len)
+            p.weights[((int64_t)t.seq * p.num_kv_heads + kh) * p.weights_stride + tok] = acc[i];
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_prefill_t(const PrefillParams& p, cudaStream_t stream) {
+    constexpr size_t smem = smem_prefill<D>();
+    cudaError_t e = cudaFuncSetAttribute(prefill_simt_kernel<T, D>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)(p.total_tokens / kB + p.num_seqs), (unsigned)p.num_heads);
+    prefill_simt_kernel<T, D><<<grid, kThreads, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_weights_t(const PrefillParams& p, cudaStream_t stream) {
+    constexpr size_t smem = sizeof(float) * (2 * (size_t)D * kPad + kB);
+    cudaError_t e = cudaFuncSetAttribute(prefill_weights_simt_kernel<T, D>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)(p.total_tokens / kB + p.num_seqs), (unsigned)p.num_kv_heads);
+    prefill_weights_simt_kernel<T, D><<<grid, kThreads, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prefill(const PrefillParams& p, int dtype, cudaStream_t stream) {
+    if (dtype == 0)
+        return p.head_dim == 64 ? launch_prefill_t<float, 64>(p, stream)
+                                : launch_prefill_t<float, 128>(p, stream);
+    return p.head_dim == 64 ? launch_prefill_t<__nv_bfloat16, 64>(p, stream)
+                            : launch_prefill_t<__nv_bfloat16, 128>(p, stream);
+}
+
+cudaError_t launch_prefill_weights(const PrefillParams& p, int dtype, cudaStream_t stream) {
+    if (dtype == 0)
+        return p.head_dim == 64 ? launch_weights_t<float, 64>(p, stream)
+                                : launch_weights_t<float, 128>(p, stream);
+    return p.head_dim == 64 ? launch_weights_t<__nv_bfloat16, 64>(p, stream)
+                            : launch_weights_t<__nv_bfloat16, 128>(p, stream);
+}
+
+cudaError_t read_status_prefill_simt(unsigned* bits, bool clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(bits, s_status_prefill_simt, sizeof(unsigned));
+    if (e != cudaSuccess || !clear || *bits == 0) return e;
+    const unsigned zero = 0;
+    return cudaMemcpyToSymbol(s_status_prefill_simt, &zero, sizeof(unsigned));
+}
+
+}  // namespace pa

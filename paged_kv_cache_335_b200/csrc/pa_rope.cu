@@ -1,0 +1,240 @@
+// pa_rope.cu — rotary positions with several axes, fused with the paged append.
+//
+// Frequency i turns the pair (x_a, x_b) of a q or k row by the angle
+//   theta_i = position[axis(i)] * inv_freq[i]
+// (rotary position embedding: Su et al., "RoFormer: Enhanced Transformer with
+// Rotary Position Embedding", eq. 34; images and video give each token a
+// position per axis, and axis(i) says which one frequency i follows), and k
+// and v then go to their cache slots as in kv_append_kernel. One pass: q, k
+// and v are read once, q_out and the slots written once; k is never written
+// back in between.
+//
+// The angle is formed as a fraction of a turn in 64-bit fixed point: turns[i] =
+// inv_freq[i] / (2 pi) modulo 1, in units of 2^-64, times the integer position,
+// modulo 2^64. That reduction loses nothing to the position's size (the error
+// is at most |position| * 2^-65 turns), where a 32-bit float product of a
+// position near 10^5 would be off by 10^-2 radians. sincospif takes the top 32
+// bits.
+//
+// Bound by HBM for prompts and by launch latency for a decode step, so: every
+// thread moves units of 16 elements (32 bytes of bf16), the loads of up to
+// kUnroll units are in flight before the table of cosines is needed, and the
+// table (one entry per token and frequency) is computed once per CTA for all
+// heads.
+#include <math.h>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+static __device__ unsigned int s_status_rope;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 3;
+constexpr int kMaxTokens = 4;   // tokens per CTA
+constexpr int kMaxHalf = 64;    // frequencies
+
+// 16 elements of a row: two pieces of 8 that lie `second` elements apart.
+struct Unit {
+    int token;      // within the CTA; -1: none
+    int row;        // 0 .. H-1: q, H .. H+Hkv-1: k, then v
+    int at;         // first element
+    int second;     // offset of the other eight
+    int freq;       // first frequency, -1: copied unchanged
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
+    if constexpr (sizeof(T) == 4) {
+        float a[4], b[4];
+        Elem<float>::widen(ld_stream(p), a);
+        Elem<float>::widen(ld_stream(p + 4), b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = a[i], f[4 + i] = b[i];
+    } else {
+        Elem<__nv_bfloat16>::widen(ld_stream(p), f);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
+    if constexpr (sizeof(T) == 4) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = (uint32_t)float_to_bf16_bits(f[2 * i]) |
+                   ((uint32_t)float_to_bf16_bits(f[2 * i + 1]) << 16);
+        st_v4(p, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+}
+
+// Eight codes of x / scale (binary32 division), as the quantising append forms
+// them: FP8 E4M3 rounded to nearest even and saturated, or int8 clamped to
+// +-127 then rounded to nearest even.
+template <int FMT>
+__device__ __forceinline__ void store8_codes(uint8_t* p, const float (&f)[8], float sc) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = __fdiv_rn(f[4 * i + j], sc);
+        if (FMT == 2)
+            w[i] = e4m3x2_code(y[0], y[1]) | (e4m3x2_code(y[2], y[3]) << 16);
+        else
+            w[i] = int8_code(y[0]) | (int8_code(y[1]) << 8) | (int8_code(y[2]) << 16) |
+                   (int8_code(y[3]) << 24);
+    }
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+
+// grid = (token groups, parts of a token's rows). T: type of q, k, v and q_out;
+// FMT: 0 / 1 = the caches hold T, 2 / 3 = E4M3 / int8 codes.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kThreads)
+rope_append_kernel(const __grid_constant__ RopeParams p) {
+    __shared__ float2 table[kMaxTokens][kMaxHalf];
+    const int token0 = blockIdx.x * p.tokens_per_cta;
+    const int ntok = min(p.tokens_per_cta, p.num_tokens - token0);
+    const int upr = p.head_dim / 16;                       // units per row
+    const int rows = p.num_heads + 2 * p.num_kv_heads;
+    const int rot_units = p.half / 8;
+    const int part = (rows * upr + gridDim.y - 1) / gridDim.y;
+    const int u0 = blockIdx.y * part, per_token = min(part, rows * upr - u0);
+    const int total = per_token > 0 ? per_token * ntok : 0;
+
+    Unit un[kUnroll];
+    float a[kUnroll][8], b[kUnroll][8];
+    auto load = [&](int base) {
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+            const int idx = base + k * kThreads + threadIdx.x;
+            un[k].token = -1;
+            if (idx >= total) continue;
+            const int tk = idx / per_token;
+            const int u = u0 + idx - tk * per_token;
+            const int row = u / upr, c = u - row * upr;
+            un[k].token = tk;
+            un[k].row = row;
+            const bool turned = row < p.num_heads + p.num_kv_heads && c < rot_units;
+            un[k].freq = turned ? 8 * c : -1;
+            un[k].at = turned && !p.adjacent ? 8 * c : 16 * c;
+            un[k].second = turned && !p.adjacent ? p.half : 8;
+            const int64_t t = token0 + tk;
+            const T* src;
+            if (row < p.num_heads)
+                src = static_cast<const T*>(p.q) + t * p.q_stride + (int64_t)row * p.head_dim;
+            else if (row < p.num_heads + p.num_kv_heads)
+                src = static_cast<const T*>(p.k) + t * p.k_stride +
+                      (int64_t)(row - p.num_heads) * p.head_dim;
+            else
+                src = static_cast<const T*>(p.v) + t * p.v_stride +
+                      (int64_t)(row - p.num_heads - p.num_kv_heads) * p.head_dim;
+            load8<T>(src + un[k].at, a[k]);
+            load8<T>(src + un[k].at + un[k].second, b[k]);
+        }
+    };
+    load(0);
+    for (int i = threadIdx.x; i < ntok * p.half; i += kThreads) {
+        const int tk = i / p.half, f = i - tk * p.half;
+        const int32_t pos = __ldg(p.positions + (int64_t)p.axis[f] * p.num_tokens + token0 + tk);
+        const uint64_t turn = (uint64_t)(int64_t)pos * p.turns[f];
+        float s, c;
+        sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
+        table[tk][f] = make_float2(c * p.mscale, s * p.mscale);
+    }
+    __syncthreads();
+    for (int base = 0; base < total; base += kUnroll * kThreads) {
+        if (base > 0) load(base);
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+            if (un[k].token < 0) continue;
+            if (un[k].freq >= 0) {
+                const float2* cs = &table[un[k].token][un[k].freq];
+                if (p.adjacent) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 w = cs[j], y = cs[4 + j];
+                        const float x0 = a[k][2 * j], x1 = a[k][2 * j + 1];
+                        const float z0 = b[k][2 * j], z1 = b[k][2 * j + 1];
+                        a[k][2 * j] = x0 * w.x - x1 * w.y;
+                        a[k][2 * j + 1] = x1 * w.x + x0 * w.y;
+                        b[k][2 * j] = z0 * y.x - z1 * y.y;
+                        b[k][2 * j + 1] = z1 * y.x + z0 * y.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 w = cs[j];
+                        const float x0 = a[k][j], x1 = b[k][j];
+                        a[k][j] = x0 * w.x - x1 * w.y;
+                        b[k][j] = x1 * w.x + x0 * w.y;
+                    }
+                }
+            }
+            const int64_t t = token0 + un[k].token;
+            int row = un[k].row;
+            if (row < p.num_heads) {
+                T* dst = static_cast<T*>(p.q_out) + (t * p.num_heads + row) * p.head_dim + un[k].at;
+                store8<T>(dst, a[k]);
+                store8<T>(dst + un[k].second, b[k]);
+                continue;
+            }
+            row -= p.num_heads;
+            const bool is_v = row >= p.num_kv_heads;
+            if (is_v) row -= p.num_kv_heads;
+            const int64_t slot = __ldg(p.slot_mapping + t);
+            if (slot < 0) continue;  // padding token
+            if (slot >= p.num_slots) {
+                atomicOr(&s_status_rope, kStatusBadIndex);
+                continue;
+            }
+            const int64_t blk = slot >> p.log2_block_size;
+            const int64_t off = slot & (p.block_size - 1);
+            const int64_t at = ((blk * p.num_kv_heads + row) * p.block_size + off) * p.head_dim + un[k].at;
+            if constexpr (FMT >= 2) {
+                uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + at;
+                const float sc = __ldg((is_v ? p.v_scale : p.k_scale) + row);
+                store8_codes<FMT>(dst, a[k], sc);
+                store8_codes<FMT>(dst + un[k].second, b[k], sc);
+            } else {
+                T* dst = static_cast<T*>(is_v ? p.v_cache : p.k_cache) + at;
+                store8<T>(dst, a[k]);
+                store8<T>(dst + un[k].second, b[k]);
+            }
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_rope_append(RopeParams p, int dtype, cudaStream_t stream) {
+    const int units = (p.num_heads + 2 * p.num_kv_heads) * (p.head_dim / 16);
+    // Many tokens: several per CTA, so the table is one entry per thread. A
+    // decode step: a token's rows over several CTAs, one unit per thread.
+    p.tokens_per_cta = p.num_tokens >= 2 * 148 * kMaxTokens ? kMaxTokens : 1;
+    const unsigned parts = p.tokens_per_cta > 1 ? 1u : (unsigned)((units + kThreads - 1) / kThreads);
+    const dim3 grid((unsigned)((p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta), parts);
+    switch (dtype) {
+        case 0: rope_append_kernel<float, 0><<<grid, kThreads, 0, stream>>>(p); break;
+        case 1: rope_append_kernel<__nv_bfloat16, 1><<<grid, kThreads, 0, stream>>>(p); break;
+        case 2: rope_append_kernel<__nv_bfloat16, 2><<<grid, kThreads, 0, stream>>>(p); break;
+        default: rope_append_kernel<__nv_bfloat16, 3><<<grid, kThreads, 0, stream>>>(p); break;
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t read_status_rope(unsigned* bits, bool clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(bits, s_status_rope, sizeof(unsigned));
+    if (e != cudaSuccess || !clear || *bits == 0) return e;
+    const unsigned zero = 0;
+    return cudaMemcpyToSymbol(s_status_rope, &zero, sizeof(unsigned));
+}
+
+}  // namespace pa
