@@ -132,6 +132,23 @@ int make_cache_map(CUtensorMap* map, const void* base, const pa_cache_desc* c) {
     return PA_OK;
 }
 
+// Packed rows [tokens][heads][head_dim] of bf16, `stride` elements between tokens, in
+// boxes of 128 tokens x 1 head x 128 bytes with the 128-byte swizzle.
+int make_rows_map(CUtensorMap* map, const void* base, int32_t tokens, int32_t heads,
+                  int32_t head_dim, int64_t stride) {
+    auto fn = encode_fn();
+    if (!fn) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64u, 1u, 128u};
+    cuuint32_t estr[3] = {1u, 1u, 1u};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return PA_OK;
+}
+
 constexpr int kMaxPartitions = 4096;
 constexpr int kAutoPartition = 512;    // CUDA-core kernel: partition when splitting
 constexpr double kMmaItemOverhead = 8.0; // tensor-core kernel: per-item cost, in 16-token sub-tiles
@@ -944,7 +961,18 @@ int pa_prefill(void* out, const void* q, const void* k, const void* v, int64_t q
     p.v = v;
     p.v_stride = v_stride;
     p.lse = lse;
-    cudaError_t ce = pa::launch_prefill(p, dtype, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t ce;
+    if (dtype == PA_F32) {
+        ce = pa::launch_prefill_simt(p, st);
+    } else {
+        CUtensorMap qmap, kmap, vmap;
+        if ((rc = make_rows_map(&qmap, q, total_tokens, num_heads, head_dim, q_stride)) != PA_OK ||
+            (rc = make_rows_map(&kmap, k, total_tokens, num_kv_heads, head_dim, k_stride)) != PA_OK ||
+            (rc = make_rows_map(&vmap, v, total_tokens, num_kv_heads, head_dim, v_stride)) != PA_OK)
+            return rc;
+        ce = pa::launch_prefill(p, qmap, kmap, vmap, st);
+    }
     return ce == cudaSuccess ? PA_OK : fail_cuda(ce, "pa_prefill launch");
 }
 
@@ -980,7 +1008,15 @@ int pa_prefill_weights(float* weights, int64_t weights_stride, const void* q, co
     cudaError_t ce = cudaMemsetAsync(weights, 0, rows * weights_stride * sizeof(float), st);
     if (ce != cudaSuccess) return fail_cuda(ce, "pa_prefill_weights memset");
     if (total_tokens == 0 || max_seq_len == 0) return PA_OK;
-    ce = pa::launch_prefill_weights(p, dtype, st);
+    if (dtype == PA_F32) {
+        ce = pa::launch_prefill_weights_simt(p, st);
+    } else {
+        CUtensorMap qmap, kmap;
+        if ((rc = make_rows_map(&qmap, q, total_tokens, num_heads, head_dim, q_stride)) != PA_OK ||
+            (rc = make_rows_map(&kmap, k, total_tokens, num_kv_heads, head_dim, k_stride)) != PA_OK)
+            return rc;
+        ce = pa::launch_prefill_weights(p, qmap, kmap, st);
+    }
     return ce == cudaSuccess ? PA_OK : fail_cuda(ce, "pa_prefill_weights launch");
 }
 
@@ -1106,6 +1142,9 @@ int pa_sync_check(void* stream) {
     if ((e = pa::read_status_evict(&x, true)) != cudaSuccess)
         return fail_cuda(e, "pa_sync_check: status word");
     a |= x;
+    if ((e = pa::read_status_prefill(&x, true)) != cudaSuccess)
+        return fail_cuda(e, "pa_sync_check: status word");
+    b |= x;
     if ((e = pa::read_status_prefill_simt(&x, true)) != cudaSuccess)
         return fail_cuda(e, "pa_sync_check: status word");
     b |= x;

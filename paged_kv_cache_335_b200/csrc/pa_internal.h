@@ -119,7 +119,7 @@ struct AddWeightsParams {
 };
 
 // Attention over whole packed prompts and the weights their tokens received
-// (pa_prefill_simt.cu). Strides in elements, between tokens.
+// (pa_prefill.cu, pa_prefill_simt.cu). Strides in elements, between tokens.
 struct PrefillParams {
     void* out;                  // [T][H][D]
     const void* q;
@@ -204,8 +204,15 @@ int evict_max_context();
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
 cudaError_t launch_add_weights(const AddWeightsParams& p, cudaStream_t stream);
 
-cudaError_t launch_prefill(const PrefillParams& p, int dtype, cudaStream_t stream);
-cudaError_t launch_prefill_weights(const PrefillParams& p, int dtype, cudaStream_t stream);
+// bf16, on the tensor cores. The maps describe q, k and v as [tokens][heads][head_dim],
+// boxes of 128 tokens x 1 head x 128 bytes, 128-byte swizzle.
+cudaError_t launch_prefill(const PrefillParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                           const CUtensorMap& vmap, cudaStream_t stream);
+cudaError_t launch_prefill_weights(const PrefillParams& p, const CUtensorMap& qmap,
+                                   const CUtensorMap& kmap, cudaStream_t stream);
+// fp32, on the CUDA cores.
+cudaError_t launch_prefill_simt(const PrefillParams& p, cudaStream_t stream);
+cudaError_t launch_prefill_weights_simt(const PrefillParams& p, cudaStream_t stream);
 
 // Record `fmt` as this host thread's last error (read by pa_get_last_error)
 // and return `code`.
@@ -217,6 +224,7 @@ cudaError_t read_status_copy(unsigned* bits, bool clear);
 cudaError_t read_status_tma(unsigned* bits, bool clear);
 cudaError_t read_status_rope(unsigned* bits, bool clear);
 cudaError_t read_status_evict(unsigned* bits, bool clear);
+cudaError_t read_status_prefill(unsigned* bits, bool clear);
 cudaError_t read_status_prefill_simt(unsigned* bits, bool clear);
 
 }  // namespace pa

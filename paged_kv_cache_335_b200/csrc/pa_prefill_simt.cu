@@ -1,5 +1,5 @@
-// pa_prefill_simt.cu — prompt attention and prompt weights on the CUDA cores, with
-// fp32 arithmetic.
+// pa_prefill_simt.cu — prompt attention and prompt weights on the CUDA cores, in
+// fp32: what pa_prefill and pa_prefill_weights run for fp32 inputs.
 //
 // out[i] = softmax over t <= i of (scale q_i . k_t) applied to v, per prompt and head
 // ("PagedAttention原理详解…", § 显存消耗的三大来源, for every query of the prompt at
@@ -27,27 +27,14 @@ constexpr int kB = 64;            // queries and keys of a tile
 constexpr int kThreads = 256;
 constexpr int kPad = kB + 4;      // row of a transposed tile (floats)
 
-// Four consecutive elements, widened.
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-}
-__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-    *reinterpret_cast<uint2*>(p) =
-        make_uint2((uint32_t)float_to_bf16_bits(v.x) | ((uint32_t)float_to_bf16_bits(v.y) << 16),
-                   (uint32_t)float_to_bf16_bits(v.z) | ((uint32_t)float_to_bf16_bits(v.w) << 16));
-}
-
 // Rows [row0, row0 + 64) x D of a packed tensor, transposed to dst[d][row];
 // rows at or past `end` become zeros.
-template <int D, typename T>
-__device__ __forceinline__ void load_t(float* dst, const T* src, int64_t stride, int row0, int end) {
+template <int D>
+__device__ __forceinline__ void load_t(float* dst, const float* src, int64_t stride, int row0, int end) {
     for (int i = threadIdx.x; i < kB * (D / 4); i += kThreads) {
         const int r = i % kB, c = i / kB;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (row0 + r < end) v = load4(src + (int64_t)(row0 + r) * stride + 4 * c);
+        if (row0 + r < end) v = *reinterpret_cast<const float4*>(src + (int64_t)(row0 + r) * stride + 4 * c);
         dst[(4 * c + 0) * kPad + r] = v.x;
         dst[(4 * c + 1) * kPad + r] = v.y;
         dst[(4 * c + 2) * kPad + r] = v.z;
@@ -79,7 +66,7 @@ constexpr size_t smem_prefill() {
     return sizeof(float) * (2 * (size_t)D * kPad + (size_t)kB * D);
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads)
 prefill_simt_kernel(const PrefillParams p) {
     extern __shared__ __align__(16) float sm[];
@@ -87,17 +74,18 @@ prefill_simt_kernel(const PrefillParams p) {
     float* kt = qt + D * kPad;       // [D][kPad]; then the weights [key][kPad]
     float* vs = kt + D * kPad;       // [kB][D]
     bool bad = false;
-    const PromptTile t = prompt_tile(p, kB, blockIdx.x, true, &bad);
+    const auto tiles = [](int len) { return (len + kB - 1) / kB; };
+    const PromptTile t = prompt_tile(p, tiles, blockIdx.x, true, &bad);
     const int h = blockIdx.y;
-    if (bad && blockIdx.x == 0 && h == 0) atomicOr(&s_status_prefill_simt, kStatusBadIndex);
+    if (bad && h == 0) atomicOr(&s_status_prefill_simt, kStatusBadIndex);
     if (t.seq < 0) return;
     const int kh = h / (p.num_heads / p.num_kv_heads);
-    const T* q = static_cast<const T*>(p.q) + (int64_t)h * D;
-    const T* k = static_cast<const T*>(p.k) + (int64_t)kh * D;
-    const T* v = static_cast<const T*>(p.v) + (int64_t)kh * D;
+    const float* q = static_cast<const float*>(p.q) + (int64_t)h * D;
+    const float* k = static_cast<const float*>(p.k) + (int64_t)kh * D;
+    const float* v = static_cast<const float*>(p.v) + (int64_t)kh * D;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int end = t.start + t.len, q0 = t.tile * kB;
-    load_t<D, T>(qt, q, p.q_stride, t.start + q0, end);
+    load_t<D>(qt, q, p.q_stride, t.start + q0, end);
     float o[4][D / 16], m[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -108,12 +96,12 @@ prefill_simt_kernel(const PrefillParams p) {
     }
     for (int j0 = 0; j0 <= q0; j0 += kB) {
         __syncthreads();
-        load_t<D, T>(kt, k, p.k_stride, t.start + j0, end);
+        load_t<D>(kt, k, p.k_stride, t.start + j0, end);
         for (int i = threadIdx.x; i < kB * (D / 4); i += kThreads) {
             const int r = i / (D / 4), c = i % (D / 4);
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (t.start + j0 + r < end)
-                x = load4(v + (int64_t)(t.start + j0 + r) * p.v_stride + 4 * c);
+                x = *reinterpret_cast<const float4*>(v + (int64_t)(t.start + j0 + r) * p.v_stride + 4 * c);
             *reinterpret_cast<float4*>(vs + r * D + 4 * c) = x;
         }
         __syncthreads();
@@ -174,11 +162,12 @@ prefill_simt_kernel(const PrefillParams p) {
         const int row = q0 + 4 * ty + i;
         if (row >= t.len) continue;
         const float inv = 1.f / l[i];
-        T* dst = static_cast<T*>(p.out) + ((int64_t)(t.start + row) * p.num_heads + h) * D;
+        float* dst = static_cast<float*>(p.out) + ((int64_t)(t.start + row) * p.num_heads + h) * D;
 #pragma unroll
         for (int g = 0; g < D / 64; ++g)
-            store4(dst + 64 * g + 4 * tx, make_float4(o[i][4 * g] * inv, o[i][4 * g + 1] * inv,
-                                                      o[i][4 * g + 2] * inv, o[i][4 * g + 3] * inv));
+            *reinterpret_cast<float4*>(dst + 64 * g + 4 * tx) =
+                make_float4(o[i][4 * g] * inv, o[i][4 * g + 1] * inv, o[i][4 * g + 2] * inv,
+                            o[i][4 * g + 3] * inv);
         if (p.lse != nullptr && tx == 0)
             p.lse[(int64_t)h * p.total_tokens + t.start + row] = (m[i] + log2f(l[i])) * 0.6931471805599453f;
     }
@@ -187,7 +176,7 @@ prefill_simt_kernel(const PrefillParams p) {
 // weights[s][kh][t] = sum over the heads of the group and the queries i >= t of
 // exp(scale q_i . k_t - lse_i): CTA = 64 keys of one kv head against tiles of 64
 // queries. Every sum is formed in a fixed order.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads)
 prefill_weights_simt_kernel(const PrefillParams p) {
     extern __shared__ __align__(16) float sm[];
@@ -195,23 +184,24 @@ prefill_weights_simt_kernel(const PrefillParams p) {
     float* qt = kt + D * kPad;
     float* lq = qt + D * kPad;       // [kB] log-sum-exp of the queries, log2 units
     bool bad = false;
-    const PromptTile t = prompt_tile(p, kB, blockIdx.x, false, &bad);
+    const auto tiles = [](int len) { return (len + kB - 1) / kB; };
+    const PromptTile t = prompt_tile(p, tiles, blockIdx.x, false, &bad);
     const int kh = blockIdx.y;
-    if (bad && blockIdx.x == 0 && kh == 0) atomicOr(&s_status_prefill_simt, kStatusBadIndex);
+    if (bad && kh == 0) atomicOr(&s_status_prefill_simt, kStatusBadIndex);
     if (t.seq < 0) return;
     const int group = p.num_heads / p.num_kv_heads;
-    const T* k = static_cast<const T*>(p.k) + (int64_t)kh * D;
+    const float* k = static_cast<const float*>(p.k) + (int64_t)kh * D;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int end = t.start + t.len, k0 = t.tile * kB;
     const int first = p.last_queries > 0 ? max(0, t.len - p.last_queries) : 0;
-    load_t<D, T>(kt, k, p.k_stride, t.start + k0, end);
+    load_t<D>(kt, k, p.k_stride, t.start + k0, end);
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     for (int g = 0; g < group; ++g) {
         const int h = kh * group + g;
-        const T* q = static_cast<const T*>(p.q) + (int64_t)h * D;
+        const float* q = static_cast<const float*>(p.q) + (int64_t)h * D;
         for (int i0 = max(k0, first / kB * kB); i0 < t.len; i0 += kB) {
             __syncthreads();
-            load_t<D, T>(qt, q, p.q_stride, t.start + i0, end);
+            load_t<D>(qt, q, p.q_stride, t.start + i0, end);
             if (threadIdx.x < kB) {
                 const int i = i0 + threadIdx.x;
                 lq[threadIdx.x] = i < t.len ? __ldg(p.lse + (int64_t)h * p.total_tokens + t.start + i) *
@@ -244,44 +234,38 @@ prefill_weights_simt_kernel(const PrefillParams p) {
     }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_prefill_t(const PrefillParams& p, cudaStream_t stream) {
     constexpr size_t smem = smem_prefill<D>();
-    cudaError_t e = cudaFuncSetAttribute(prefill_simt_kernel<T, D>,
+    cudaError_t e = cudaFuncSetAttribute(prefill_simt_kernel<D>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(p.total_tokens / kB + p.num_seqs), (unsigned)p.num_heads);
-    prefill_simt_kernel<T, D><<<grid, kThreads, smem, stream>>>(p);
+    // one more than there can be tiles: its CTAs look every prompt over
+    const dim3 grid((unsigned)(p.total_tokens / kB + p.num_seqs + 1), (unsigned)p.num_heads);
+    prefill_simt_kernel<D><<<grid, kThreads, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_weights_t(const PrefillParams& p, cudaStream_t stream) {
     constexpr size_t smem = sizeof(float) * (2 * (size_t)D * kPad + kB);
-    cudaError_t e = cudaFuncSetAttribute(prefill_weights_simt_kernel<T, D>,
+    cudaError_t e = cudaFuncSetAttribute(prefill_weights_simt_kernel<D>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(p.total_tokens / kB + p.num_seqs), (unsigned)p.num_kv_heads);
-    prefill_weights_simt_kernel<T, D><<<grid, kThreads, smem, stream>>>(p);
+    // one more than there can be tiles: its CTAs look every prompt over
+    const dim3 grid((unsigned)(p.total_tokens / kB + p.num_seqs + 1), (unsigned)p.num_kv_heads);
+    prefill_weights_simt_kernel<D><<<grid, kThreads, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_prefill(const PrefillParams& p, int dtype, cudaStream_t stream) {
-    if (dtype == 0)
-        return p.head_dim == 64 ? launch_prefill_t<float, 64>(p, stream)
-                                : launch_prefill_t<float, 128>(p, stream);
-    return p.head_dim == 64 ? launch_prefill_t<__nv_bfloat16, 64>(p, stream)
-                            : launch_prefill_t<__nv_bfloat16, 128>(p, stream);
+cudaError_t launch_prefill_simt(const PrefillParams& p, cudaStream_t stream) {
+    return p.head_dim == 64 ? launch_prefill_t<64>(p, stream) : launch_prefill_t<128>(p, stream);
 }
 
-cudaError_t launch_prefill_weights(const PrefillParams& p, int dtype, cudaStream_t stream) {
-    if (dtype == 0)
-        return p.head_dim == 64 ? launch_weights_t<float, 64>(p, stream)
-                                : launch_weights_t<float, 128>(p, stream);
-    return p.head_dim == 64 ? launch_weights_t<__nv_bfloat16, 64>(p, stream)
-                            : launch_weights_t<__nv_bfloat16, 128>(p, stream);
+cudaError_t launch_prefill_weights_simt(const PrefillParams& p, cudaStream_t stream) {
+    return p.head_dim == 64 ? launch_weights_t<64>(p, stream) : launch_weights_t<128>(p, stream);
 }
 
 cudaError_t read_status_prefill_simt(unsigned* bits, bool clear) {

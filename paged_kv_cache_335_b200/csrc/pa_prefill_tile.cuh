@@ -1,4 +1,5 @@
-// pa_prefill_tile.cuh — tiles of packed prompts.
+// pa_prefill_tile.cuh — tiles of packed prompts, shared by the kernels of
+// pa_prefill.cu and pa_prefill_simt.cu.
 #pragma once
 
 #include "pa_device.cuh"
@@ -6,19 +7,21 @@
 
 namespace pa {
 
-// One tile of `bm` consecutive tokens of one prompt.
+// One tile of one prompt.
 struct PromptTile {
     int seq;    // -1: the index lies behind the last tile
     int start;  // the prompt's first packed row
     int len;    // its tokens
-    int tile;   // tokens tile * bm .. of the prompt
+    int tile;   // which of the prompt's tiles
 };
 
 // Tile `u` of the packed prompts, found by a whole warp from the sequence starts (32
-// prompts per step): prompts in order, the tiles of one prompt from the last to
-// the first when `reversed`. A prompt with bad bounds (outside [0, total_tokens],
-// negative length, or longer than max_seq_len) has no tile; *bad reports it.
-__device__ __forceinline__ PromptTile prompt_tile(const PrefillParams& p, int bm, int u,
+// prompts per step): prompts in order, each with tiles(its length) tiles, counted from
+// the last to the first when `reversed`. A prompt with bad bounds (outside
+// [0, total_tokens], negative length, or longer than max_seq_len) has no tile; *bad
+// reports it.
+template <typename Tiles>
+__device__ __forceinline__ PromptTile prompt_tile(const PrefillParams& p, Tiles tiles, int u,
                                                   bool reversed, bool* bad) {
     const int lane = threadIdx.x & 31;
     PromptTile r;
@@ -36,7 +39,7 @@ __device__ __forceinline__ PromptTile prompt_tile(const PrefillParams& p, int bm
                 len = 0;
             }
         }
-        const int nt = (len + bm - 1) / bm;
+        const int nt = tiles(len);
         int x = nt;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {

@@ -156,6 +156,16 @@ def test_bad_prompts_are_skipped(dtype):
             pa.pa_sync_check()
         assert e.value.code == pa.PA_ERR_BAD_INDEX
         assert bool((out[good[0]:good[1]] != 7).all())
+    # the 40th of prompts whose tiles are all found among the first 32
+    out = torch.full(q.shape, 7.0, device=DEV, dtype=dtype)
+    w = torch.empty((40, h, 310), device=DEV)
+    cut = torch.tensor([0, 1] + [1] * 38 + [311], dtype=torch.int32, device=DEV)
+    for call in (lambda: pa.pa_prefill(out, q, k, v, cut, 0.125, max_seq_len=310),
+                 lambda: pa.pa_prefill_weights(w, q, k, torch.zeros((h, 310), device=DEV), cut, 0.125, max_seq_len=310)):
+        call()
+        with pytest.raises(pa.PAError):
+            pa.pa_sync_check()
+    assert bool((out[1:] == 7).all()) and not w[1:].any()
     out = torch.full(q.shape, 7.0, device=DEV, dtype=dtype)
     pa.pa_prefill(out, q, k, v, torch.tensor(cu, dtype=torch.int32, device=DEV), 0.125, max_seq_len=100)
     with pytest.raises(pa.PAError):
