@@ -11,12 +11,13 @@
 // a tile; a CTA takes two consecutive ones, so that both read the same K and V
 // tiles (two heads of one tile, or two tiles of one head) and one's products run while the
 // other's softmax does. Roles:
-//   warp 8: issues S_b = Q_b K^T (128 x 128, K = head_dim, A and B in shared memory)
+//   warp 16: issues S_b = Q_b K^T (128 x 128, K = head_dim, A and B in shared memory)
 //     and O_b += P_b V (A = P from TMEM, B = V read MN-major), completions by commit;
-//   warp 9: loads Q and the ring of K and V tiles by TMA;
-//   warps 0..3 and 4..7: the softmax of row blocks 0 and 1, a thread per row. P (bf16)
-//     overwrites the first half of its S in TMEM;
-//   warps 10 and 11: on the tiles that the diagonal crosses, zero the elements of V that are
+//   warp 17: loads Q and the ring of K and V tiles by TMA;
+//   warps 0..7 and 8..15: the softmax of row blocks 0 and 1, two threads per row (of warps
+//     that share TMEM lanes), which exchange the row's maximum in every tile and its sum at
+//     the end. P (bf16) overwrites the first half of its S in TMEM;
+//   warps 18 and 19: on the tiles that the diagonal crosses, zero the elements of V that are
 //     not finite, and the rows behind the prompt, before the tensor core reads
 //     them: a masked weight is 0, and 0 x infinity would not be. The epilogue adds the
 //     elements so taken out to the rows that attend to them.
@@ -50,6 +51,12 @@ constexpr int kBlk = 128;                 // tokens of a tile
 constexpr int kHalfBytes = kBlk * 128;    // 64 of a tile's head_dim elements: 128 rows x 128 bytes
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.f;
+#ifndef PA_ATTN_POLY
+#define PA_ATTN_POLY 0
+#endif
+#ifndef PA_WEIGHTS_POLY
+#define PA_WEIGHTS_POLY 2
+#endif
 
 // Bounded wait; gives up at once when another role already gave up.
 __device__ __forceinline__ bool wait_or_dead(volatile int* dead, uint32_t bar, uint32_t parity) {
@@ -90,10 +97,41 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+    return fma2(b, make_float2(-1.f, -1.f), a);
+}
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     uint32_t d;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
+}
+
+// 2^x of two values, x <= 128, on the fp32 units instead of the exponential unit: with n =
+// round(x) (by adding 1.5 x 2^23) and f = x - n in [-1/2, 1/2], 2^f by its degree-5
+// polynomial of least relative error (Remez exchange; below 2.4e-7 in fp32 arithmetic),
+// and n added to the exponent bits. x <= -127 gives 0.
+__device__ __forceinline__ float2 exp2_poly(float2 x) {
+    const float2 big = make_float2(12582912.f, 12582912.f);
+    x.x = fmaxf(x.x, -127.f);
+    x.y = fmaxf(x.y, -127.f);
+    const float2 t = add2(x, big);
+    const float2 f = add2(x, sub2(big, t));
+    auto both = [](float c) { return make_float2(c, c); };
+    float2 y = fma2(f, both(0.0013276472454890609f), both(0.009675540961325169f));
+    y = fma2(f, y, both(0.05550713092088699f));
+    y = fma2(f, y, both(0.24022120237350464f));
+    y = fma2(f, y, both(0.6931469440460205f));
+    y = fma2(f, y, both(1.0000001192092896f));
+    return make_float2(__int_as_float(__float_as_int(y.x) + (__float_as_int(t.x) << 23)),
+                       __int_as_float(__float_as_int(y.y) + (__float_as_int(t.y) << 23)));
+}
+
+// 2^x of the pair with index c of a row: kPoly of every eight pairs by polynomial, the
+// others by the exponential unit, which alone would bound the kernel.
+template <int kPoly>
+__device__ __forceinline__ float2 exp2_pair(float2 x, int c) {
+    if ((c & 7) * kPoly % 8 + kPoly > 7) return exp2_poly(x);  // spread evenly (compile time)
+    return make_float2(ex2(x.x), ex2(x.y));
 }
 
 // One tile of a packed tensor into shared memory, half by half.
@@ -105,22 +143,29 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
     for (int h = 0; h < D / 64; ++h) tma_load_3d(dst + h * kHalfBytes, map, 64 * h, head, token, bar);
 }
 
-// S = A B^T over head_dim, A and B tiles in shared memory.
+// Descriptor words of a tile: K-major (head_dim contiguous, as A or B of a product over
+// head_dim), and as V, whose product runs over the rows.
+__device__ __forceinline__ uint32_t rows_lo(uint32_t tile) { return umma_desc_lo(tile, 16); }
+__device__ __forceinline__ uint32_t v_lo(uint32_t tile) { return umma_desc_lo(tile, kHalfBytes); }
+constexpr uint32_t kDescHi = umma_desc_hi(1024);
+
+// S = A B^T over head_dim, A and B tiles in shared memory (their rows_lo).
 template <int D>
 __device__ __forceinline__ void issue_qk(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-        const uint32_t at = (k >> 2) * kHalfBytes + (k & 3) * 32;
-        umma_ss(d, umma_desc(a + at, 16, 1024), umma_desc(b + at, 16, 1024), idesc, k > 0);
+        const uint32_t at = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
+        umma_ss_words(d, a + at, b + at, kDescHi, idesc, k > 0);
     }
 }
 
 // ---------------------------------------------------------------------------
 // attention
 // ---------------------------------------------------------------------------
-constexpr int kAttnThreads = 384;
-constexpr uint32_t kAttnTmemCols = 512;   // S_0, S_1 (128 columns each), O_0, O_1
 constexpr int kCleaners = 2;              // warps
+constexpr int kSoftWarps = 16;             // eight per row block, then products, loads, cleaners
+constexpr int kAttnThreads = 32 * (kSoftWarps + 2 + kCleaners);
+constexpr uint32_t kAttnTmemCols = 512;   // S_0, S_1 (128 columns each), O_0, O_1
 
 template <int D>
 struct AttnCfg {
@@ -130,13 +175,47 @@ struct AttnCfg {
     static constexpr int kExt = kRing + kStages * kTile;
     // q 2, full S, empty S, s 2, p 2, o 2, edge 2, clean 2, fin
     static constexpr int kNumBars = 2 * kStages + 13;
-    static constexpr int kSmem = kExt + 8 * kNumBars + 16;    // + TMEM slot, dead, taken out
+    static constexpr int kXch = kExt + (8 * kNumBars + 12 + 15) / 16 * 16;  // + TMEM slot, dead, taken out
+    // a row's maxima, at the end its sums, [2 row blocks][2 halves][128]
+    static constexpr int kSmem = kXch + 4 * kBlk * 4;
     static constexpr uint32_t kColO = 256;
     static constexpr uint32_t kIdescQK = umma_idesc(kBlk, kBlk, false);
     static constexpr uint32_t kIdescPV = umma_idesc(kBlk, D, true);
     static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 constexpr uint32_t kNegateA = 1u << 13;   // of the instruction descriptor
+
+// Whether `pred` holds for any thread of the two warps that share rows (barrier `id`).
+__device__ __forceinline__ bool pair_any(int id, bool pred) {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 q, %2, 0;\n"
+                 " bar.red.or.pred p, %1, 64, q;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(r) : "r"(id), "r"((uint32_t)pred) : "memory");
+    return r != 0;
+}
+
+// The weights 2^(s sl - ms) of half a row: bf16 into TMEM at ts; returns their fp32 sum in
+// two parts.
+template <int kPoly>
+__device__ __forceinline__ float2 put_weights(const uint32_t (&s)[64], float sl, float ms, uint32_t ts) {
+    const float2 sl2 = make_float2(sl, sl), ms2 = make_float2(-ms, -ms);
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int g = 0; g < 64; g += 32) {
+        uint32_t w[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            const int at = g + 2 * c;
+            const float2 x = exp2_pair<kPoly>(
+                fma2(make_float2(__uint_as_float(s[at]), __uint_as_float(s[at + 1])), sl2, ms2), c);
+            w[c] = bf16x2(x.x, x.y);
+            sum[c & 1] = add2(sum[c & 1], x);
+        }
+        tmem_st16_issue(ts + g / 2, w);
+    }
+    tmem_wait_st();
+    return add2(sum[0], sum[1]);
+}
 
 template <int D>
 __global__ void __launch_bounds__(kAttnThreads, 1)
@@ -163,7 +242,6 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     const int blocks = (u.len + kBlk - 1) / kBlk * group;
     const int nb = min(2, blocks - 2 * u.tile);
     const int tile0 = 2 * u.tile / group, tile1 = (2 * u.tile + nb - 1) / group;
-    const int nk[2] = {tile0 + 1, nb == 2 ? tile1 + 1 : 0};   // key tiles of each
     const int nkmax = tile1 + 1;
 
     uint8_t* ext = smem + C::kExt;
@@ -183,7 +261,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         for (int i = 0; i < 2; ++i) {
             mbar_init(b_q + 8 * i, 1);
             mbar_init(b_s + 8 * i, 1);
-            mbar_init(b_p + 8 * i, 4);
+            mbar_init(b_p + 8 * i, kSoftWarps / 2);
             mbar_init(b_o + 8 * i, 1);
             mbar_init(b_edge + 8 * i, 1);
             mbar_init(b_clean + 8 * i, kCleaners);
@@ -193,48 +271,63 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         *taken = 0;
         fence_barrier_init();
     }
-    if (warp == 8) tmem_alloc(smem_u32(tslot), kAttnTmemCols);
+    if (warp == kSoftWarps) tmem_alloc(smem_u32(tslot), kAttnTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = *tslot;
 
-    if (warp < 8) {  // softmax of row block b, a thread per row
-        const int b = warp >> 2;
-        if (nk[b] > 0) {
+    // 640 threads get 96 registers each: the 512 of the softmax take 104, the others 64
+    if (warp < kSoftWarps)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp < kSoftWarps) {  // softmax of row block b: half a row per thread
+        const int b = warp >> 3, half = (warp >> 2) & 1, row = threadIdx.x & 127;
+        if (b < nb) {
+            const int last = b ? tile1 : tile0;   // key tile on the diagonal
             const int head = kh * group + (2 * u.tile + b) % group;
-            const int qi = (b ? tile1 : tile0) * kBlk + (threadIdx.x & 127);
+            const int qi = last * kBlk + row;
+            const int pair_id = 1 + 4 * b + (warp & 3);
             const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-            const uint32_t ts = tm + lanes + 128 * b, to = tm + lanes + C::kColO + D * b;
+            const uint32_t ts = tm + lanes + 128 * b, to = tm + lanes + C::kColO + D * b + D / 2 * half;
+            float* xch = reinterpret_cast<float*>(smem + C::kXch) + 2 * kBlk * b + row;
             // (its sign is in the product; not 0, so that a masked -infinity stays one)
             const float sl = fmaxf(fabsf(p.scale_log2), 1e-30f);
             float m = -INFINITY, ms = 0.f;
             float2 l2 = make_float2(0.f, 0.f);
             bool ok = true;
-            for (int j = 0; j < nk[b]; ++j) {
-                if (!(ok = __all_sync(0xffffffffu, wait_or_dead(dead, b_s + 8 * b, j & 1)))) break;
-                tc_fence_after();
-                uint32_t s0[64], s1[64];
-                tmem_ld64_issue(ts, s0);
-                tmem_ld64_issue(ts + 64, s1);
-                tmem_wait_ld(s0);
-                tmem_wait_ld(s1);
-                if (j == nk[b] - 1) {  // the tile the diagonal crosses
-                    const int lim = qi - j * kBlk;
+            for (int j = 0; j <= last; ++j) {
+                ok = __all_sync(0xffffffffu, wait_or_dead(dead, b_s + 8 * b, j & 1));
+                uint32_t s[64];
+                float mt = -INFINITY;
+                if (ok) {
+                    tc_fence_after();
+                    tmem_ld64_issue(ts + 64 * half, s);
+                    tmem_wait_ld(s);
+                    if (j == last) {  // the tile the diagonal crosses
+                        const int lim = qi - j * kBlk - 64 * half;
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) {
-                        if (c > lim) s0[c] = 0xff800000u;
-                        if (c + 64 > lim) s1[c] = 0xff800000u;
+                        for (int c = 0; c < 64; ++c)
+                            if (c > lim) s[c] = 0xff800000u;
                     }
-                }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 64; c += 4) {
+                    for (int c = 0; c < 64; c += 8)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(s0[c + i])), __uint_as_float(s1[c + i]));
+                        for (int i = 0; i < 4; ++i)
+                            mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(s[c + i])), __uint_as_float(s[c + 4 + i]));
+                    mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    // (the other thread has read the last one: it did so before its weights,
+                    // which S_b's product waited for)
+                    xch[half * kBlk] = mt;
                 }
-                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                // both halves are in registers (P may overwrite S) and their maxima known
+                if (pair_any(pair_id, !ok)) {
+                    ok = false;
+                    break;
+                }
+                mt = fmaxf(mt, xch[(half ^ 1) * kBlk]);
                 if (j == 0) {
                     m = mt;
                     ms = m * sl;
@@ -250,56 +343,36 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                         l2.x *= al;
                         l2.y *= al;
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(to + c, o);
+                        for (int c = 0; c < D / 2; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(to + c, o);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-                            tmem_st32_issue(to + c, o);
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                            tmem_st16(to + c, o);
                         }
-                        tmem_wait_st();
                     }
                 }
-                const float2 sl2 = make_float2(sl, sl), ms2 = make_float2(-ms, -ms);
-                float2 add = make_float2(0.f, 0.f);
-                uint32_t w[32];
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    float2 x = fma2(make_float2(__uint_as_float(s0[2 * c]), __uint_as_float(s0[2 * c + 1])), sl2, ms2);
-                    x.x = ex2(x.x);
-                    x.y = ex2(x.y);
-                    w[c] = bf16x2(x.x, x.y);
-                    add = add2(add, x);
-                }
-                tmem_st32_issue(ts, w);
-                float2 add_b = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    float2 x = fma2(make_float2(__uint_as_float(s1[2 * c]), __uint_as_float(s1[2 * c + 1])), sl2, ms2);
-                    x.x = ex2(x.x);
-                    x.y = ex2(x.y);
-                    w[c] = bf16x2(x.x, x.y);
-                    add_b = add2(add_b, x);
-                }
-                tmem_st32_issue(ts + 32, w);
-                tmem_wait_st();
+                if (j == last)
+                    l2 = add2(l2, put_weights<0>(s, sl, ms, ts + 32 * half));
+                else
+                    l2 = add2(l2, put_weights<PA_ATTN_POLY>(s, sl, ms, ts + 32 * half));
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_p + 8 * b);
-                l2 = add2(l2, add2(add, add_b));
             }
             if (ok) ok = wait_or_dead(dead, b_o + 8 * b, 0);
             // (and the cleaners' note, for the fix below)
             for (int c = 0; ok && c <= tile1 - tile0; ++c) ok = wait_or_dead(dead, b_clean + 8 * c, 0);
-            ok = __all_sync(0xffffffffu, ok);
-            if (ok) {
+            if (ok) xch[half * kBlk] = l2.x + l2.y;
+            if (!pair_any(pair_id, !ok)) {
                 tc_fence_after();
-                const float l = l2.x + l2.y, inv = 1.f / l;
+                const float l = xch[0] + xch[kBlk], inv = 1.f / l;
                 const bool live = qi < u.len;
                 const bool fix = *taken != 0;
-                uint16_t* dst = static_cast<uint16_t*>(p.out) + ((int64_t)(u.start + qi) * p.num_heads + head) * D;
+                uint16_t* dst = static_cast<uint16_t*>(p.out) +
+                                ((int64_t)(u.start + qi) * p.num_heads + head) * D + D / 2 * half;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
+                for (int c = 0; c < D / 2; c += 32) {
                     uint32_t o[32];
                     __syncwarp();
                     tmem_ld32(to + c, o);
@@ -311,7 +384,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                         for (int t = tile0 * kBlk; t <= qi; ++t) {
                             const uint4* src = reinterpret_cast<const uint4*>(
                                 static_cast<const uint16_t*>(p.v) + (int64_t)(u.start + t) * p.v_stride +
-                                (int64_t)kh * D + c);
+                                (int64_t)kh * D + D / 2 * half + c);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 float x[8];
@@ -328,58 +401,82 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                               make_uint4(bf16x2(f[8 * i], f[8 * i + 1]), bf16x2(f[8 * i + 2], f[8 * i + 3]),
                                          bf16x2(f[8 * i + 4], f[8 * i + 5]), bf16x2(f[8 * i + 6], f[8 * i + 7])));
                 }
-                if (live && p.lse != nullptr)
+                if (live && half == 0 && p.lse != nullptr)
                     p.lse[(int64_t)head * p.total_tokens + u.start + qi] = (ms + log2f(l)) * kLn2;
             }
         }
-    } else if (warp == 8) {  // products
-        if (lane == 0) {
-            const uint32_t idqk = C::kIdescQK | (p.scale_log2 < 0.f ? kNegateA : 0u);
-            auto stage = [&](int i) { return ring + (i % S_) * C::kTile; };
-            auto full = [&](int i) { return wait_or_dead(dead, b_full + 8 * (i % S_), (i / S_) & 1); };
-            bool ok = true;
-            for (int b = 0; b < nb && ok; ++b) {
-                if (!(ok = wait_or_dead(dead, b_q + 8 * b, 0) && (b > 0 || full(0)))) break;
-                issue_qk<D>(tm + 128 * b, qbuf + b * C::kTile, stage(0), idqk);
+    } else if (warp == kSoftWarps) {  // products
+        // The whole warp walks the tiles (what the descriptors are made of stays warp-uniform);
+        // one thread issues.
+        const uint32_t idqk = C::kIdescQK | (p.scale_log2 < 0.f ? kNegateA : 0u);
+        const bool one = elect_one();
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, wait_or_dead(dead, bar, parity));
+        };
+        // S_b from the K tile in stage st
+        auto qk = [&](int b, int st) {
+            const uint32_t q_lo = rows_lo(qbuf + b * C::kTile), k_lo = rows_lo(ring + st * C::kTile);
+            if (one) {
+                issue_qk<D>(tm + kBlk * b, q_lo, k_lo, idqk);
                 umma_commit(b_s + 8 * b);
             }
-            if (ok) umma_commit(b_empty);
-            for (int j = 0; j < nkmax && ok; ++j) {
-                const int iv = 2 * j + 1, ik = 2 * j + 2;
-                bool have_v = false, have_k = false;
-                for (int b = 0; b < nb && ok; ++b) {
-                    if (j >= nk[b]) continue;
-                    if (!have_v) {
-                        ok = j >= tile0 ? wait_or_dead(dead, b_clean + 8 * (j - tile0), 0) : full(iv);
-                        have_v = true;
-                    }
-                    if (!ok || !(ok = wait_or_dead(dead, b_p + 8 * b, j & 1))) break;
-                    tc_fence_after();
+            __syncwarp();
+        };
+        bool ok = true;
+        for (int b = 0; b < nb && ok; ++b) {
+            ok = wait(b_q + 8 * b, 0) && (b > 0 || wait(b_full, 0));
+            if (ok) qk(b, 0);
+        }
+        if (ok && one) umma_commit(b_empty);
+        __syncwarp();
+        // ring place (stage, parity) of V tile j, and of K tile j + 1 behind it
+        int sv = 1, sk = 2;
+        uint32_t pv = 0, pk = 0;
+        for (int j = 0; j < nkmax && ok; ++j) {
+            bool have_v = false, have_k = false;
+            for (int b = 0; b < nb && ok; ++b) {
+                const int last = (b ? tile1 : tile0);   // key tile on the diagonal
+                if (j > last) continue;
+                if (!have_v) {
+                    ok = j >= tile0 ? wait(b_clean + 8 * (j - tile0), 0) : wait(b_full + 8 * sv, pv);
+                    have_v = true;
+                }
+                if (!ok || !(ok = wait(b_p + 8 * b, j & 1))) break;
+                tc_fence_after();
+                const uint32_t lo = v_lo(ring + sv * C::kTile);
+                if (one) {
 #pragma unroll
                     for (int k = 0; k < kBlk / 16; ++k)
-                        umma_ts(tm + C::kColO + D * b, tm + 128 * b + 8 * k,
-                                umma_desc(stage(iv) + 2048 * k, kHalfBytes, 1024), C::kIdescPV, j > 0 || k > 0);
-                    if (j == nk[b] - 1) {
-                        umma_commit(b_o + 8 * b);
-                        continue;
-                    }
+                        umma_ts_words(tm + C::kColO + D * b, tm + kBlk * b + 8 * k, lo + 128 * k, kDescHi,
+                                      C::kIdescPV, k > 0 || j > 0);
+                    if (j == last) umma_commit(b_o + 8 * b);
+                }
+                __syncwarp();
+                if (j < last) {
                     if (!have_k) {
-                        if (!(ok = full(ik))) break;
+                        if (!(ok = wait(b_full + 8 * sk, pk))) break;
                         have_k = true;
                     }
-                    issue_qk<D>(tm + 128 * b, qbuf + b * C::kTile, stage(ik), idqk);
-                    umma_commit(b_s + 8 * b);
-                }
-                if (ok) {
-                    umma_commit(b_empty + 8 * (iv % S_));
-                    if (have_k) umma_commit(b_empty + 8 * (ik % S_));
+                    qk(b, sk);
                 }
             }
-            // every product issued here is complete before TMEM is freed
-            umma_commit(b_fin);
-            if (!mbar_wait_bounded(b_fin, 0)) atomicOr(&s_status_prefill, kStatusTimeout);
+            if (ok) {
+                if (one) {
+                    umma_commit(b_empty + 8 * sv);
+                    if (have_k) umma_commit(b_empty + 8 * sk);
+                }
+                __syncwarp();
+                for (int n = 0; n < 2; ++n) {
+                    if (++sv == S_) sv = 0, pv ^= 1;
+                    if (++sk == S_) sk = 0, pk ^= 1;
+                }
+            }
         }
-    } else if (warp == 9) {  // loads
+        // every product issued here is complete before TMEM is freed
+        if (one) umma_commit(b_fin);
+        __syncwarp();
+        if (!mbar_wait_bounded(b_fin, 0)) atomicOr(&s_status_prefill, kStatusTimeout);
+    } else if (warp == kSoftWarps + 1) {  // loads
         if (lane == 0) {
             prefetch_tensormap(&qmap);
             prefetch_tensormap(&kmap);
@@ -414,7 +511,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             }
         }
     } else {  // cleaners
-        const int t = threadIdx.x - 320;
+        const int t = threadIdx.x - 32 * (kSoftWarps + 2);
         for (int c = 0; c <= tile1 - tile0; ++c) {
             const int j = tile0 + c;
             if (!__all_sync(0xffffffffu, wait_or_dead(dead, b_edge + 8 * c, 0))) break;
@@ -452,7 +549,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tm, kAttnTmemCols);
+    if (warp == kSoftWarps) tmem_dealloc(tm, kAttnTmemCols);
 }
 
 // ---------------------------------------------------------------------------
@@ -581,12 +678,8 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
                                         make_float2(e.x, e.y));
                         float2 y = fma2(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), sl2,
                                         make_float2(e.z, e.w));
-                        x.x = ex2(x.x);
-                        x.y = ex2(x.y);
-                        y.x = ex2(y.x);
-                        y.y = ex2(y.y);
-                        acc[0] = add2(acc[0], x);
-                        acc[1] = add2(acc[1], y);
+                        acc[0] = add2(acc[0], exp2_pair<PA_WEIGHTS_POLY>(x, c / 2));
+                        acc[1] = add2(acc[1], exp2_pair<PA_WEIGHTS_POLY>(y, c / 2 + 1));
                     }
                 } else {
 #pragma unroll
@@ -601,20 +694,31 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
         if (ok && key < u.len)
             p.weights[((int64_t)u.seq * p.num_kv_heads + kh) * p.weights_stride + key] = sum;
     } else if (warp == 4) {  // products
-        if (lane == 0) {
-            const uint32_t idesc = umma_idesc(kBlk, kBlk, false) | (p.scale_log2 < 0.f ? kNegateA : 0u);
-            bool ok = wait_or_dead(dead, b_k, 0);
-            for (int n = 0; n < steps && ok; ++n) {
-                if (n >= 2 && !(ok = wait_or_dead(dead, b_free + 8 * (n & 1), ((n >> 1) & 1) ^ 1))) break;
-                if (!(ok = wait_or_dead(dead, b_full + 8 * (n % S_), (n / S_) & 1))) break;
-                tc_fence_after();
-                issue_qk<D>(tm + 128 * (n & 1), raw, raw + C::kRing + (n % S_) * C::kTile, idesc);
+        const uint32_t idesc = umma_idesc(kBlk, kBlk, false) | (p.scale_log2 < 0.f ? kNegateA : 0u);
+        const bool one = elect_one();
+        const uint32_t k_lo = rows_lo(raw);
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, wait_or_dead(dead, bar, parity));
+        };
+        bool ok = wait(b_k, 0);
+        int st = 0;
+        uint32_t ph = 0;
+        for (int n = 0; n < steps && ok; ++n) {
+            if (n >= 2 && !(ok = wait(b_free + 8 * (n & 1), ((n >> 1) & 1) ^ 1))) break;
+            if (!(ok = wait(b_full + 8 * st, ph))) break;
+            tc_fence_after();
+            const uint32_t d = tm + kBlk * (n & 1), q_lo = rows_lo(raw + C::kRing + st * C::kTile);
+            if (one) {
+                issue_qk<D>(d, k_lo, q_lo, idesc);
                 umma_commit(b_s + 8 * (n & 1));
-                umma_commit(b_empty + 8 * (n % S_));
+                umma_commit(b_empty + 8 * st);
             }
-            umma_commit(b_fin);
-            if (!mbar_wait_bounded(b_fin, 0)) atomicOr(&s_status_prefill, kStatusTimeout);
+            __syncwarp();
+            if (++st == S_) st = 0, ph ^= 1;
         }
+        if (one) umma_commit(b_fin);
+        __syncwarp();
+        if (!mbar_wait_bounded(b_fin, 0)) atomicOr(&s_status_prefill, kStatusTimeout);
     } else if (lane == 0) {  // loads
         load_tile<D>(raw, &kmap, kh, u.start + key0, b_k);
         bool ok = true;
