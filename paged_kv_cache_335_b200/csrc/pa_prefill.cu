@@ -8,12 +8,12 @@
 //
 // Attention. A row block is 128 consecutive tokens of one prompt under one head. The
 // row blocks of a kv head are counted tile by tile, the heads of its group inside
-// a tile; a CTA takes two consecutive ones, so that both read the same K and V
+// a tile; an item is two consecutive ones, so that both read the same K and V
 // tiles (two heads of one tile, or two tiles of one head) and one's products run while the
-// other's softmax does. Roles:
+// other's softmax does. Roles of a CTA:
 //   warp 16: issues S_b = Q_b K^T (128 x 128, K = head_dim, A and B in shared memory)
 //     and O_b += P_b V (A = P from TMEM, B = V read MN-major), completions by commit;
-//   warp 17: loads Q and the ring of K and V tiles by TMA;
+//   warp 17: loads Q and the ring of K and V tiles by TMA, and finds the next item;
 //   warps 0..7 and 8..15: the softmax of row blocks 0 and 1, two threads per row (of warps
 //     that share TMEM lanes), which exchange the row's maximum in every tile and its sum at
 //     the end. P (bf16) overwrites the first half of its S in TMEM;
@@ -24,15 +24,22 @@
 // The weights are 2^(score - m) with m a reference that moves only when a row's
 // maximum exceeds it by more than 2^kRescaleLog2 (numerator and denominator share it, so
 // the result is the exact softmax); O is then rescaled in TMEM by its row's own
-// thread. What a row does depends on its own scores alone. P is rounded to bf16 for
+// threads. What a row does depends on its own scores alone. P is rounded to bf16 for
 // the product (an operand of the tensor core); its sum takes the fp32 weights.
 //
 // Weights. weights[t] = sum over heads of the group and queries i >= t of
 // 2^(score - lse_i): S^T = K Q^T with the keys as rows, so that a key's sum stays in one
-// thread; query tiles stream past one key tile. Two CTAs per SM.
+// thread (two: query tiles in turn); query tiles stream past one key tile. A part of the exponentials runs on the fp32 units.
 //
-// Bound by the tensor cores (2 x 1024 cycles per tile pair and row block at head_dim 128)
-// and the exponential unit (16 per cycle and SM: 1024 cycles per 128 x 128 weights) alike.
+// Both kernels stay on their SM and take item after item: the grid is one CTA per item, and a
+// running CTA cancels the launch of one that has not started and does its work
+// (cluster launch control), so that the next item's tiles load while this one's
+// epilogue runs, and long and short prompts balance without a counter in memory.
+//
+// Bound by the tensor cores (64 cycles per 128 x 128 x 16 product: 1024 per key tile and
+// row block at head_dim 128), the exponential unit (16 per cycle and SM: 1024 cycles per
+// 128 x 128 weights) and, in between, by the chain S -> softmax -> P V -> next S of a row
+// block, which the other row block only partly covers.
 #include <math.h>
 
 #include "pa_device.cuh"
@@ -51,12 +58,6 @@ constexpr int kBlk = 128;                 // tokens of a tile
 constexpr int kHalfBytes = kBlk * 128;    // 64 of a tile's head_dim elements: 128 rows x 128 bytes
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.f;
-#ifndef PA_ATTN_POLY
-#define PA_ATTN_POLY 0
-#endif
-#ifndef PA_WEIGHTS_POLY
-#define PA_WEIGHTS_POLY 2
-#endif
 
 // Bounded wait; gives up at once when another role already gave up.
 __device__ __forceinline__ bool wait_or_dead(volatile int* dead, uint32_t bar, uint32_t parity) {
@@ -134,6 +135,16 @@ __device__ __forceinline__ float2 exp2_pair(float2 x, int c) {
     return make_float2(ex2(x.x), ex2(x.y));
 }
 
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 x) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                 :: "r"(addr), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+}
+// Bits 15 and 31: whether the lower and upper bf16 of a word are infinite or NaN (an exponent
+// of all ones, to which one more unit carries into the sign's place).
+__device__ __forceinline__ uint32_t odd_bf16(uint32_t w) {
+    return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+
 // One tile of a packed tensor into shared memory, half by half.
 template <int D>
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int head, int token,
@@ -160,10 +171,158 @@ __device__ __forceinline__ void issue_qk(uint32_t d, uint32_t a, uint32_t b, uin
 }
 
 // ---------------------------------------------------------------------------
+// items
+// ---------------------------------------------------------------------------
+// What a CTA works on next: one (prompt, kv head, tile), decoded by the loading warp.
+struct Item {
+    int seq;    // kNothing: the index lies behind the last one; kEnd: no more
+    int start, len, tile, kh;
+};
+constexpr int kNothing = -1, kEnd = -2;
+
+// Shared-memory places of the hand-over of items: four slots in turn.
+constexpr int kSlots = 4;
+struct ItemBars {
+    uint32_t full, empty, answer;  // [kSlots], [kSlots], and of the launch control's answer
+    volatile int* slots;           // [kSlots][8]
+    uint32_t response;             // 16 bytes
+};
+constexpr int kItemBars = 2 * kSlots + 1, kItemBytes = 32 * kSlots + 16;
+
+// Ask for the launch of a pending CTA to be cancelled; the answer (16 bytes) completes on bar.
+__device__ __forceinline__ void ask_next(uint32_t response, uint32_t bar) {
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 :: "r"(response), "r"(bar) : "memory");
+}
+// The cancelled CTA's index, or -1: none was left.
+__device__ __forceinline__ int answer_index(uint32_t response) {
+    uint32_t yes, x;
+    asm volatile("{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\tld.shared.b128 h, [%2];\n\t"
+                 "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+                 "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, h;\n\t}"
+                 : "=r"(yes), "=r"(x) : "r"(response) : "memory");
+    return yes ? (int)x : -1;
+}
+
+// The loading warp: hands over the item with index `id`, loads it by load(item) (false: gave
+// up), and goes on with the next.
+template <typename Tiles, typename Load>
+__device__ __forceinline__ void walk_items(const PrefillParams& p, const ItemBars& ib, volatile int* dead,
+                                           bool reversed, Tiles tiles, Load load) {
+    const int lane = threadIdx.x & 31;
+    int id = blockIdx.x;
+    PromptWalk walk;
+    for (int n = 0;; ++n) {
+        Item it;
+        it.seq = kEnd;
+        if (id >= 0) {
+            it.kh = id % p.num_kv_heads;
+            const PromptTile u = walk.find(p, tiles, id / p.num_kv_heads, reversed);
+            it.seq = u.seq;
+            it.start = u.start;
+            it.len = u.len;
+            it.tile = u.tile;
+            if (walk.bad) {
+                atomicOr(&s_status_prefill, kStatusBadIndex);
+                walk.bad = false;
+            }
+        }
+        const int slot = n % kSlots;
+        if (n >= kSlots &&
+            !__all_sync(0xffffffffu, wait_or_dead(dead, ib.empty + 8 * slot, ((n / kSlots) & 1) ^ 1)))
+            return;
+        if (lane == 0) {
+            volatile int* d = ib.slots + 8 * slot;
+            d[0] = it.seq;
+            if (it.seq >= 0) {
+                d[1] = it.start;
+                d[2] = it.len;
+                d[3] = it.tile;
+                d[4] = it.kh;
+            }
+            mbar_arrive(ib.full + 8 * slot);
+            if (id >= 0) ask_next(ib.response, ib.answer);
+        }
+        __syncwarp();
+        if (id < 0) return;
+        const bool ok = it.seq < 0 || __all_sync(0xffffffffu, load(it));
+        // (also after a give-up: the answer is on its way into shared memory)
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(ib.answer, n & 1))) {
+            if (lane == 0) atomicOr(&s_status_prefill, kStatusTimeout);
+            *dead = 1;
+            return;
+        }
+        if (!ok) return;
+        id = answer_index(ib.response);
+        __syncwarp();
+        fence_async_smem();  // the answer is read before the next one is written
+    }
+}
+
+// The other warps: the n-th item; seq = kEnd after the last or a give-up. Its slot holds
+// until leave_item.
+__device__ __forceinline__ Item peek_item(const ItemBars& ib, int n) {
+    const volatile int* d = ib.slots + 8 * (n % kSlots);
+    Item it;
+    it.seq = d[0];
+    it.start = d[1];
+    it.len = d[2];
+    it.tile = d[3];
+    it.kh = d[4];
+    return it;
+}
+__device__ __forceinline__ bool wait_item(const ItemBars& ib, volatile int* dead, int n) {
+    return __all_sync(0xffffffffu, wait_or_dead(dead, ib.full + 8 * (n % kSlots), (n / kSlots) & 1));
+}
+__device__ __forceinline__ void leave_item(const ItemBars& ib, int n) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(ib.empty + 8 * (n % kSlots));
+}
+__device__ __forceinline__ Item take_item(const ItemBars& ib, volatile int* dead, int n) {
+    Item it;
+    it.seq = kEnd;
+    if (!wait_item(ib, dead, n)) return it;
+    it = peek_item(ib, n);
+    leave_item(ib, n);
+    return it;
+}
+
+__device__ __forceinline__ ItemBars item_bars(uint32_t bars, uint8_t* bytes, int takers) {
+    ItemBars ib;
+    ib.full = bars;
+    ib.empty = bars + 8 * kSlots;
+    ib.answer = bars + 16 * kSlots;
+    ib.response = smem_u32(bytes);
+    ib.slots = reinterpret_cast<volatile int*>(bytes + 16);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(ib.full + 8 * i, 1);
+            mbar_init(ib.empty + 8 * i, takers);
+        }
+        mbar_init(ib.answer, 1);
+    }
+    return ib;
+}
+
+// A place in a ring of S stages: stage and the parity of its present use.
+template <int S>
+struct Place {
+    int st = 0;
+    uint32_t par = 0;
+    __device__ __forceinline__ Place next() const {
+        Place r = *this;
+        if (++r.st == S) r.st = 0, r.par ^= 1;
+        return r;
+    }
+};
+
+// ---------------------------------------------------------------------------
 // attention
 // ---------------------------------------------------------------------------
 constexpr int kCleaners = 2;              // warps
-constexpr int kSoftWarps = 16;             // eight per row block, then products, loads, cleaners
+constexpr int kSoftWarps = 16;            // eight per row block, then products, loads, cleaners
 constexpr int kAttnThreads = 32 * (kSoftWarps + 2 + kCleaners);
 constexpr uint32_t kAttnTmemCols = 512;   // S_0, S_1 (128 columns each), O_0, O_1
 
@@ -172,18 +331,31 @@ struct AttnCfg {
     static constexpr int kTile = D / 64 * kHalfBytes;
     static constexpr int kStages = D == 128 ? 5 : 8;          // K and V tiles, alternating
     static constexpr int kRing = 2 * kTile;                   // after the two Q tiles
-    static constexpr int kExt = kRing + kStages * kTile;
-    // q 2, full S, empty S, s 2, p 2, o 2, edge 2, clean 2, fin
-    static constexpr int kNumBars = 2 * kStages + 13;
-    static constexpr int kXch = kExt + (8 * kNumBars + 12 + 15) / 16 * 16;  // + TMEM slot, dead, taken out
     // a row's maxima, at the end its sums, [2 row blocks][2 halves][128]
-    static constexpr int kSmem = kXch + 4 * kBlk * 4;
+    static constexpr int kXch = kRing + kStages * kTile;
+    static constexpr int kItems = kXch + 4 * kBlk * 4;
+    static constexpr int kBars = kItems + kItemBytes;
+    // q 2, its release 2, full S, empty S, s 2, p 2, o 2, note 2, edge 2, clean 2, fin
+    static constexpr int kNumBars = 2 * kStages + 17 + kItemBars;
+    static constexpr int kSmem = kBars + 8 * kNumBars + 32;   // + TMEM slot, dead, taken 4, noted 2
     static constexpr uint32_t kColO = 256;
     static constexpr uint32_t kIdescQK = umma_idesc(kBlk, kBlk, false);
     static constexpr uint32_t kIdescPV = umma_idesc(kBlk, D, true);
     static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 constexpr uint32_t kNegateA = 1u << 13;   // of the instruction descriptor
+
+// Row blocks 2 tile and 2 tile + 1 of a kv head (the last one of an odd count is alone): how
+// many, and the token tiles of both, which are also their last key tiles.
+struct Blocks {
+    int nb, tile0, tile1;
+    __device__ __forceinline__ Blocks(const Item& it, int group) {
+        nb = min(2, (it.len + kBlk - 1) / kBlk * group - 2 * it.tile);
+        tile0 = 2 * it.tile / group;
+        tile1 = (2 * it.tile + nb - 1) / group;
+    }
+    __device__ __forceinline__ int last(int b) const { return b ? tile1 : tile0; }
+};
 
 // Whether `pred` holds for any thread of the two warps that share rows (barrier `id`).
 __device__ __forceinline__ bool pair_any(int id, bool pred) {
@@ -196,7 +368,6 @@ __device__ __forceinline__ bool pair_any(int id, bool pred) {
 
 // The weights 2^(s sl - ms) of half a row: bf16 into TMEM at ts; returns their fp32 sum in
 // two parts.
-template <int kPoly>
 __device__ __forceinline__ float2 put_weights(const uint32_t (&s)[64], float sl, float ms, uint32_t ts) {
     const float2 sl2 = make_float2(sl, sl), ms2 = make_float2(-ms, -ms);
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -206,8 +377,9 @@ __device__ __forceinline__ float2 put_weights(const uint32_t (&s)[64], float sl,
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
             const int at = g + 2 * c;
-            const float2 x = exp2_pair<kPoly>(
-                fma2(make_float2(__uint_as_float(s[at]), __uint_as_float(s[at + 1])), sl2, ms2), c);
+            float2 x = fma2(make_float2(__uint_as_float(s[at]), __uint_as_float(s[at + 1])), sl2, ms2);
+            x.x = ex2(x.x);
+            x.y = ex2(x.y);
             w[c] = bf16x2(x.x, x.y);
             sum[c & 1] = add2(sum[c & 1], x);
         }
@@ -226,32 +398,20 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = p.num_heads / p.num_kv_heads;
-    const int kh = blockIdx.x % p.num_kv_heads;
-    bool bad = false;
-    const PromptTile u = prompt_tile(
-        p, [group](int len) { return ((len + kBlk - 1) / kBlk * group + 1) / 2; },
-        blockIdx.x / p.num_kv_heads, true, &bad);
-    if (bad && kh == 0) atomicOr(&s_status_prefill, kStatusBadIndex);
-    if (u.seq < 0) return;
     const uint32_t raw = smem_u32(smem);
     if (raw & 1023u) {
         if (threadIdx.x == 0) atomicOr(&s_status_prefill, kStatusSmemAlign);
         return;
     }
-    // row blocks 2 u.tile and 2 u.tile + 1 (the last one of an odd count is alone)
-    const int blocks = (u.len + kBlk - 1) / kBlk * group;
-    const int nb = min(2, blocks - 2 * u.tile);
-    const int tile0 = 2 * u.tile / group, tile1 = (2 * u.tile + nb - 1) / group;
-    const int nkmax = tile1 + 1;
-
-    uint8_t* ext = smem + C::kExt;
-    const uint32_t bars = smem_u32(ext);
-    const uint32_t b_q = bars, b_full = b_q + 16, b_empty = b_full + 8 * S_, b_s = b_empty + 8 * S_,
-                   b_p = b_s + 16, b_o = b_p + 16, b_edge = b_o + 16, b_clean = b_edge + 16,
-                   b_fin = b_clean + 16;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(ext + 8 * C::kNumBars);
+    const uint32_t bars = smem_u32(smem + C::kBars);
+    const uint32_t b_q = bars, b_qfree = b_q + 16, b_full = b_qfree + 16, b_empty = b_full + 8 * S_,
+                   b_s = b_empty + 8 * S_, b_p = b_s + 16, b_o = b_p + 16, b_note = b_o + 16,
+                   b_edge = b_note + 16, b_clean = b_edge + 16, b_fin = b_clean + 16;
+    const ItemBars ib = item_bars(b_fin + 8, smem + C::kItems, kSoftWarps + 1 + kCleaners);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBars + 8 * C::kNumBars);
     volatile int* dead = reinterpret_cast<volatile int*>(tslot + 1);
-    volatile int* taken = reinterpret_cast<volatile int*>(tslot + 2);
+    volatile int* taken = dead + 1;   // [2 edge slots][cleaners]: elements were zeroed
+    volatile int* noted = taken + 2 * kCleaners;   // [2] of a row block: in one of its item's edge tiles
     const uint32_t qbuf = raw, ring = raw + C::kRing;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S_; ++i) {
@@ -260,15 +420,16 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(b_q + 8 * i, 1);
+            mbar_init(b_qfree + 8 * i, 1);
             mbar_init(b_s + 8 * i, 1);
             mbar_init(b_p + 8 * i, kSoftWarps / 2);
             mbar_init(b_o + 8 * i, 1);
+            mbar_init(b_note + 8 * i, 1);
             mbar_init(b_edge + 8 * i, 1);
             mbar_init(b_clean + 8 * i, kCleaners);
         }
         mbar_init(b_fin, 1);
         *dead = 0;
-        *taken = 0;
         fence_barrier_init();
     }
     if (warp == kSoftWarps) tmem_alloc(smem_u32(tslot), kAttnTmemCols);
@@ -276,6 +437,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = *tslot;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_or_dead(dead, bar, parity));
+    };
 
     // 640 threads get 96 registers each: the 512 of the softmax take 104, the others 64
     if (warp < kSoftWarps)
@@ -284,21 +448,29 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp < kSoftWarps) {  // softmax of row block b: half a row per thread
         const int b = warp >> 3, half = (warp >> 2) & 1, row = threadIdx.x & 127;
-        if (b < nb) {
-            const int last = b ? tile1 : tile0;   // key tile on the diagonal
-            const int head = kh * group + (2 * u.tile + b) % group;
-            const int qi = last * kBlk + row;
-            const int pair_id = 1 + 4 * b + (warp & 3);
-            const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-            const uint32_t ts = tm + lanes + 128 * b, to = tm + lanes + C::kColO + D * b + D / 2 * half;
-            float* xch = reinterpret_cast<float*>(smem + C::kXch) + 2 * kBlk * b + row;
-            // (its sign is in the product; not 0, so that a masked -infinity stays one)
-            const float sl = fmaxf(fabsf(p.scale_log2), 1e-30f);
+        const int pair_id = 1 + 4 * b + (warp & 3);
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t ts = tm + lanes + kBlk * b, to = tm + lanes + C::kColO + D * b + D / 2 * half;
+        float* xch = reinterpret_cast<float*>(smem + C::kXch) + 2 * kBlk * b + row;
+        // (its sign is in the product; not 0, so that a masked -infinity stays one)
+        const float sl = fmaxf(fabsf(p.scale_log2), 1e-30f);
+        uint32_t par_s = 0, par_o = 0;
+        bool ok = true;
+        for (int n = 0; ok; ++n, leave_item(ib, n - 1)) {
+            if (!wait_item(ib, dead, n)) break;
+            const int seq = ib.slots[8 * (n % kSlots)];
+            if (seq == kEnd) break;
+            if (seq < 0) continue;
+            int last;      // the row block's last key tile: the one on the diagonal
+            {
+                const Blocks k(peek_item(ib, n), group);
+                if (b >= k.nb) continue;
+                last = k.last(b);
+            }
             float m = -INFINITY, ms = 0.f;
             float2 l2 = make_float2(0.f, 0.f);
-            bool ok = true;
-            for (int j = 0; j <= last; ++j) {
-                ok = __all_sync(0xffffffffu, wait_or_dead(dead, b_s + 8 * b, j & 1));
+            for (int j = 0; j <= last; ++j, par_s ^= 1) {
+                ok = wait(b_s + 8 * b, par_s);
                 uint32_t s[64];
                 float mt = -INFINITY;
                 if (ok) {
@@ -306,7 +478,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                     tmem_ld64_issue(ts + 64 * half, s);
                     tmem_wait_ld(s);
                     if (j == last) {  // the tile the diagonal crosses
-                        const int lim = qi - j * kBlk - 64 * half;
+                        const int lim = row - 64 * half;
 #pragma unroll
                         for (int c = 0; c < 64; ++c)
                             if (c > lim) s[c] = 0xff800000u;
@@ -352,124 +524,161 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                         }
                     }
                 }
-                if (j == last)
-                    l2 = add2(l2, put_weights<0>(s, sl, ms, ts + 32 * half));
-                else
-                    l2 = add2(l2, put_weights<PA_ATTN_POLY>(s, sl, ms, ts + 32 * half));
+                l2 = add2(l2, put_weights(s, sl, ms, ts + 32 * half));
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_p + 8 * b);
             }
-            if (ok) ok = wait_or_dead(dead, b_o + 8 * b, 0);
-            // (and the cleaners' note, for the fix below)
-            for (int c = 0; ok && c <= tile1 - tile0; ++c) ok = wait_or_dead(dead, b_clean + 8 * c, 0);
+            if (ok) ok = wait(b_o + 8 * b, par_o) && wait(b_note + 8 * b, par_o);
+            par_o ^= 1;
             if (ok) xch[half * kBlk] = l2.x + l2.y;
-            if (!pair_any(pair_id, !ok)) {
-                tc_fence_after();
-                const float l = xch[0] + xch[kBlk], inv = 1.f / l;
-                const bool live = qi < u.len;
-                const bool fix = *taken != 0;
-                uint16_t* dst = static_cast<uint16_t*>(p.out) +
-                                ((int64_t)(u.start + qi) * p.num_heads + head) * D + D / 2 * half;
+            if (pair_any(pair_id, !ok)) break;
+            tc_fence_after();
+            const float l = xch[0] + xch[kBlk], inv = 1.f / l;
+            const Item it = peek_item(ib, n);
+            const Blocks k(it, group);
+            const int qi = last * kBlk + row;
+            const bool live = qi < it.len;
+            const int head = it.kh * group + (2 * it.tile + b) % group;
+            uint16_t* out = static_cast<uint16_t*>(p.out) +
+                            ((int64_t)it.start * p.num_heads + head) * D + D / 2 * half;
+            const int64_t out_stride = (int64_t)p.num_heads * D;
+            const int row0 = qi - (lane & 3);   // the first row of this thread's four lanes
 #pragma unroll 1
-                for (int c = 0; c < D / 2; c += 32) {
-                    uint32_t o[32];
-                    __syncwarp();
-                    tmem_ld32(to + c, o);
-                    if (!live) continue;
-                    float f[32];
+            for (int c = 0; c < D / 2; c += 32) {
+                uint32_t o[32];
+                __syncwarp();
+                tmem_ld32(to + c, o);
+                uint32_t w[16];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * inv;
-                    if (fix) {
-                        for (int t = tile0 * kBlk; t <= qi; ++t) {
-                            const uint4* src = reinterpret_cast<const uint4*>(
-                                static_cast<const uint16_t*>(p.v) + (int64_t)(u.start + t) * p.v_stride +
-                                (int64_t)kh * D + D / 2 * half + c);
+                for (int i = 0; i < 16; ++i)
+                    w[i] = bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                // a row per thread would touch a line per thread in each store: four lanes exchange
+                // their 16-byte chunks, so that a store writes 64 bytes of each of eight rows
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                float x[8];
-                                Elem<__nv_bfloat16>::widen(ld_v4(src + i), x);
+                for (int mask = 1; mask < 4; mask <<= 1) {
+                    const bool up = lane & mask;
 #pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    if (!(fabsf(x[e]) < INFINITY)) f[8 * i + e] += x[e];
-                            }
-                        }
+                    for (int i = 0; i < 16; ++i) {
+                        if ((i >> 2) & mask) continue;
+                        uint32_t &lo = w[i], &hi = w[i + 4 * mask];
+                        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, mask);
+                        if (up)
+                            lo = got;
+                        else
+                            hi = got;
                     }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        st_v4(dst + c + 8 * i,
-                              make_uint4(bf16x2(f[8 * i], f[8 * i + 1]), bf16x2(f[8 * i + 2], f[8 * i + 3]),
-                                         bf16x2(f[8 * i + 4], f[8 * i + 5]), bf16x2(f[8 * i + 6], f[8 * i + 7])));
                 }
-                if (live && half == 0 && p.lse != nullptr)
-                    p.lse[(int64_t)head * p.total_tokens + u.start + qi] = (ms + log2f(l)) * kLn2;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (row0 + i < it.len)
+                        st_v4(out + (row0 + i) * out_stride + c + 8 * (lane & 3),
+                              make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
             }
+            if (noted[b] != 0) {
+                // elements of V taken out of the edge tiles: infinite or NaN, they add to
+                // whatever the row holds
+                __syncwarp();
+                for (int t = k.tile0 * kBlk; live && t <= qi; ++t) {
+                    const uint16_t* v = static_cast<const uint16_t*>(p.v) + (int64_t)(it.start + t) * p.v_stride +
+                                        (int64_t)it.kh * D + D / 2 * half;
+#pragma unroll 1
+                    for (int c = 0; c < D / 2; ++c) {
+                        const float x = bf16_lo(v[c]);
+                        uint16_t* at = out + qi * out_stride + c;
+                        if (!(fabsf(x) < INFINITY)) *at = float_to_bf16_bits(bf16_lo(*at) + x);
+                    }
+                }
+            }
+            if (live && half == 0 && p.lse != nullptr)
+                p.lse[(int64_t)head * p.total_tokens + it.start + qi] = (ms + log2f(l)) * kLn2;
+            __syncwarp();
+            tc_fence_before();               // O is read before the next item's first PV
+            named_barrier(pair_id, 64);      // and the sums before its first maxima
         }
     } else if (warp == kSoftWarps) {  // products
         // The whole warp walks the tiles (what the descriptors are made of stays warp-uniform);
         // one thread issues.
         const uint32_t idqk = C::kIdescQK | (p.scale_log2 < 0.f ? kNegateA : 0u);
         const bool one = elect_one();
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, wait_or_dead(dead, bar, parity));
-        };
+        Place<S_> cur;                      // of the next K tile
+        uint32_t par_q[2] = {0, 0}, par_p[2] = {0, 0};
+        int edges = 0;
+        bool ok = true;
         // S_b from the K tile in stage st
-        auto qk = [&](int b, int st) {
+        auto qk = [&](int b, int st, bool last) {
             const uint32_t q_lo = rows_lo(qbuf + b * C::kTile), k_lo = rows_lo(ring + st * C::kTile);
             if (one) {
                 issue_qk<D>(tm + kBlk * b, q_lo, k_lo, idqk);
                 umma_commit(b_s + 8 * b);
+                if (last) umma_commit(b_qfree + 8 * b);
             }
             __syncwarp();
         };
-        bool ok = true;
-        for (int b = 0; b < nb && ok; ++b) {
-            ok = wait(b_q + 8 * b, 0) && (b > 0 || wait(b_full, 0));
-            if (ok) qk(b, 0);
-        }
-        if (ok && one) umma_commit(b_empty);
-        __syncwarp();
-        // ring place (stage, parity) of V tile j, and of K tile j + 1 behind it
-        int sv = 1, sk = 2;
-        uint32_t pv = 0, pk = 0;
-        for (int j = 0; j < nkmax && ok; ++j) {
-            bool have_v = false, have_k = false;
-            for (int b = 0; b < nb && ok; ++b) {
-                const int last = (b ? tile1 : tile0);   // key tile on the diagonal
-                if (j > last) continue;
-                if (!have_v) {
-                    ok = j >= tile0 ? wait(b_clean + 8 * (j - tile0), 0) : wait(b_full + 8 * sv, pv);
-                    have_v = true;
-                }
-                if (!ok || !(ok = wait(b_p + 8 * b, j & 1))) break;
-                tc_fence_after();
-                const uint32_t lo = v_lo(ring + sv * C::kTile);
-                if (one) {
+        for (int n = 0; ok; ++n) {
+            const Item it = take_item(ib, dead, n);
+            if (it.seq == kEnd) break;
+            if (it.seq < 0) continue;
+            const Blocks k(it, group);
 #pragma unroll
-                    for (int k = 0; k < kBlk / 16; ++k)
-                        umma_ts_words(tm + C::kColO + D * b, tm + kBlk * b + 8 * k, lo + 128 * k, kDescHi,
-                                      C::kIdescPV, k > 0 || j > 0);
-                    if (j == last) umma_commit(b_o + 8 * b);
-                }
-                __syncwarp();
-                if (j < last) {
-                    if (!have_k) {
-                        if (!(ok = wait(b_full + 8 * sk, pk))) break;
-                        have_k = true;
-                    }
-                    qk(b, sk);
-                }
+            for (int b = 0; b < 2; ++b) {
+                if (b >= k.nb || !ok) continue;
+                ok = wait(b_q + 8 * b, par_q[b]) && (b > 0 || wait(b_full + 8 * cur.st, cur.par));
+                par_q[b] ^= 1;
+                if (ok) qk(b, cur.st, k.last(b) == 0);
             }
-            if (ok) {
-                if (one) {
-                    umma_commit(b_empty + 8 * sv);
-                    if (have_k) umma_commit(b_empty + 8 * sk);
+            if (!ok) break;
+            if (one) umma_commit(b_empty + 8 * cur.st);
+            __syncwarp();
+            int note = 0;
+            for (int j = 0; j <= k.tile1 && ok; ++j) {
+                const Place<S_> pv = cur.next(), pk = pv.next();
+                bool have_v = false, have_k = false;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    if (b >= k.nb || j > k.last(b) || !ok) continue;
+                    if (!have_v) {
+                        have_v = true;
+                        if (j >= k.tile0) {
+                            ok = wait(b_clean + 8 * (edges & 1), (edges >> 1) & 1);
+                            if (ok)
+                                for (int c = 0; c < kCleaners; ++c) note |= taken[(edges & 1) * kCleaners + c];
+                            ++edges;
+                        } else {
+                            ok = wait(b_full + 8 * pv.st, pv.par);
+                        }
+                    }
+                    if (!ok || !(ok = wait(b_p + 8 * b, par_p[b]))) continue;
+                    par_p[b] ^= 1;
+                    tc_fence_after();
+                    const uint32_t lo = v_lo(ring + pv.st * C::kTile);
+                    const bool last = j == k.last(b);
+                    if (one) {
+#pragma unroll
+                        for (int i = 0; i < kBlk / 16; ++i)
+                            umma_ts_words(tm + C::kColO + D * b, tm + kBlk * b + 8 * i, lo + 128 * i, kDescHi,
+                                          C::kIdescPV, i > 0 || j > 0);
+                        if (last) {
+                            umma_commit(b_o + 8 * b);
+                            noted[b] = note;
+                            mbar_arrive(b_note + 8 * b);
+                        }
+                    }
+                    __syncwarp();
+                    if (!last) {
+                        if (!have_k) {
+                            if (!(ok = wait(b_full + 8 * pk.st, pk.par))) continue;
+                            have_k = true;
+                        }
+                        qk(b, pk.st, j + 1 == k.last(b));
+                    }
+                }
+                if (ok && one) {
+                    umma_commit(b_empty + 8 * pv.st);
+                    if (have_k) umma_commit(b_empty + 8 * pk.st);
                 }
                 __syncwarp();
-                for (int n = 0; n < 2; ++n) {
-                    if (++sv == S_) sv = 0, pv ^= 1;
-                    if (++sk == S_) sk = 0, pk ^= 1;
-                }
+                cur = pk;
             }
         }
         // every product issued here is complete before TMEM is freed
@@ -481,68 +690,112 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             prefetch_tensormap(&qmap);
             prefetch_tensormap(&kmap);
             prefetch_tensormap(&vmap);
-            auto load_q = [&](int b) {
-                load_tile<D>(qbuf + b * C::kTile, &qmap, kh * group + (2 * u.tile + b) % group,
-                             u.start + (b ? tile1 : tile0) * kBlk, b_q + 8 * b);
-            };
-            // Tile i of the ring: K (even) or V (odd) of key tile i / 2. The V tiles that
-            // the diagonal crosses complete on barriers of their own; nothing is
-            // loaded into their stages after them.
-            bool ok = true;
-            int issued = 0;
-            for (int i = 0; i < 2 * nkmax; ++i) {
-                const int st = i % S_, j = i >> 1;
-                if (i >= S_ && !(ok = wait_or_dead(dead, b_empty + 8 * st, ((i / S_) & 1) ^ 1))) break;
-                if (i == 0) load_q(0);
-                const bool v = i & 1;
-                load_tile<D>(ring + st * C::kTile, v ? &vmap : &kmap, kh, u.start + j * kBlk,
-                             v && j >= tile0 ? b_edge + 8 * (j - tile0) : b_full + 8 * st);
-                if (i == 0 && nb == 2) load_q(1);
-                issued = i + 1;
-            }
-            if (!ok) {  // given up: the loads in flight land before the CTA ends
-                bool landed = mbar_wait_bounded(b_q, 0) && (nb < 2 || mbar_wait_bounded(b_q + 8, 0));
-                for (int i = max(0, issued - S_); i < issued; ++i) {
-                    const int j = i >> 1;
-                    landed &= (i & 1) && j >= tile0 ? mbar_wait_bounded(b_edge + 8 * (j - tile0), 0)
-                                                    : mbar_wait_bounded(b_full + 8 * (i % S_), (i / S_) & 1);
+        }
+        Place<S_> at;
+        int loaded = 0;                    // tiles of the ring
+        int used_q[2] = {0, 0}, edges = 0, edge_at[2] = {0, 0};
+        walk_items(
+            p, ib, dead, true, [group](int len) { return ((len + kBlk - 1) / kBlk * group + 1) / 2; },
+            [&](const Item& it) {
+                bool ok = true;
+                if (lane == 0) {
+                    const Blocks k(it, group);
+                    auto load_q = [&](int b) {
+                        if (used_q[b] > 0 && !wait_or_dead(dead, b_qfree + 8 * b, (used_q[b] - 1) & 1)) return false;
+                        ++used_q[b];
+                        load_tile<D>(qbuf + b * C::kTile, &qmap, it.kh * group + (2 * it.tile + b) % group,
+                                     it.start + k.last(b) * kBlk, b_q + 8 * b);
+                        return true;
+                    };
+                    // K (even) or V (odd) of key tile i / 2
+                    for (int i = 0; i < 2 * (k.tile1 + 1) && ok; ++i, ++loaded, at = at.next()) {
+                        if (loaded >= S_ && !(ok = wait_or_dead(dead, b_empty + 8 * at.st, at.par ^ 1))) break;
+                        if (i == 0 && !(ok = load_q(0))) break;
+                        const int j = i >> 1;
+                        const bool edge = (i & 1) && j >= k.tile0;
+                        if (edge) {
+                            // the tile that used this edge slot before has been released, so
+                            // nobody still waits for that use's phases
+                            const int before = edge_at[edges & 1];
+                            if (edges >= 2 && before + S_ > loaded &&
+                                !(ok = wait_or_dead(dead, b_empty + 8 * (before % S_), (before / S_) & 1)))
+                                break;
+                        }
+                        load_tile<D>(ring + at.st * C::kTile, i & 1 ? &vmap : &kmap, it.kh, it.start + j * kBlk,
+                                     b_full + 8 * at.st);
+                        if (edge) {
+                            mbar_arrive(b_edge + 8 * (edges & 1));
+                            edge_at[edges & 1] = loaded;
+                            ++edges;
+                        }
+                        if (i == 0 && k.nb == 2) ok = load_q(1);
+                    }
                 }
-                if (!landed) atomicOr(&s_status_prefill, kStatusTimeout);
-            }
+                __syncwarp();
+                return ok;
+            });
+        if (lane == 0 && *dead != 0) {  // given up: the loads in flight land before the CTA ends
+            bool landed = true;
+            for (int b = 0; b < 2; ++b)
+                if (used_q[b] > 0) landed &= mbar_wait_bounded(b_q + 8 * b, (used_q[b] - 1) & 1);
+            for (int i = max(0, loaded - S_); i < loaded; ++i)
+                landed &= mbar_wait_bounded(b_full + 8 * (i % S_), (i / S_) & 1);
+            if (!landed) atomicOr(&s_status_prefill, kStatusTimeout);
         }
     } else {  // cleaners
         const int t = threadIdx.x - 32 * (kSoftWarps + 2);
-        for (int c = 0; c <= tile1 - tile0; ++c) {
-            const int j = tile0 + c;
-            if (!__all_sync(0xffffffffu, wait_or_dead(dead, b_edge + 8 * c, 0))) break;
-            const uint32_t buf = ring + ((2 * j + 1) % S_) * C::kTile;
-            const int rows = u.len - j * kBlk;  // of the prompt
-            bool found = false;
-#pragma unroll 4
-            for (int i = t; i < D / 64 * kBlk * 8; i += 32 * kCleaners) {
-                const int r = (i >> 3) & (kBlk - 1);
-                const uint32_t at = buf + 16 * i;  // (a row's eight chunks, in whatever order)
-                uint4 x = lds128(at);
-                uint32_t* xw = &x.x;
-                bool odd = r >= rows;
+        Place<S_> at;
+        int edges = 0;
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            const Item it = take_item(ib, dead, n);
+            if (it.seq == kEnd) break;
+            if (it.seq < 0) continue;
+            const Blocks k(it, group);
+            for (int j = 0; j <= k.tile1 && ok; ++j) {
+                at = at.next();  // V of key tile j
+                if (j >= k.tile0) {
+                    const int slot = edges & 1;
+                    // the load is under way (so `full` is in its phase), then landed
+                    ok = wait(b_edge + 8 * slot, (edges >> 1) & 1) && wait(b_full + 8 * at.st, at.par);
+                    ++edges;
+                    if (!ok) break;
+                    const uint32_t buf = ring + at.st * C::kTile;
+                    const int rows = it.len - j * kBlk;  // of the prompt
+                    constexpr int kChunks = D / 64 * kBlk * 8 / (32 * kCleaners);   // per thread
+                    uint32_t found = 0;
+#pragma unroll 8
+                    for (int i = 0; i < kChunks; ++i) {
+                        const int c = t + 32 * kCleaners * i;  // (a row's eight chunks, in whatever order)
+                        const int r = (c >> 3) & (kBlk - 1);
+                        const uint4 x = lds128(buf + 16 * c);
+                        if (r >= rows)
+                            sts128(buf + 16 * c, make_uint4(0u, 0u, 0u, 0u));
+                        else
+                            found |= odd_bf16(x.x) | odd_bf16(x.y) | odd_bf16(x.z) | odd_bf16(x.w);
+                    }
+                    if (found) {  // take the elements out of this thread's chunks
+                        for (int i = 0; i < kChunks; ++i) {
+                            const int c = t + 32 * kCleaners * i;
+                            uint4 x = lds128(buf + 16 * c);
+                            uint32_t* w = &x.x;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    // an exponent of all ones: infinite or NaN
-                    const bool lo = (xw[e] & 0x7f80u) == 0x7f80u, hi = (xw[e] & 0x7f800000u) == 0x7f800000u;
-                    if (lo) xw[e] &= 0xffff0000u;
-                    if (hi) xw[e] &= 0x0000ffffu;
-                    odd |= lo | hi;
-                    found |= (lo | hi) && r < rows;
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t odd = odd_bf16(w[e]);
+                                if (odd & 0x8000u) w[e] &= 0xffff0000u;
+                                if (odd & 0x80000000u) w[e] &= 0x0000ffffu;
+                            }
+                            sts128(buf + 16 * c, x);
+                        }
+                    }
+                    const bool any = __any_sync(0xffffffffu, found != 0);
+                    if (lane == 0) taken[slot * kCleaners + (t >> 5)] = any;
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(b_clean + 8 * slot);
                 }
-                if (r >= rows) x = make_uint4(0u, 0u, 0u, 0u);
-                if (odd)
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
-                                 :: "r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+                at = at.next();
             }
-            if (found) *taken = 1;
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b_clean + 8 * c);
         }
     }
     __syncwarp();
@@ -555,23 +808,41 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
 // ---------------------------------------------------------------------------
 // weights
 // ---------------------------------------------------------------------------
-constexpr int kWThreads = 192;            // four warps that sum, products, loads
-constexpr uint32_t kWTmemCols = 256;      // S^T twice
+constexpr int kSumWarps = 8;              // two groups of four, then products, loads
+constexpr int kWThreads = 32 * (kSumWarps + 2);
+constexpr int kWBufs = 4;                 // of S^T
+constexpr uint32_t kWTmemCols = kWBufs * kBlk;
+#ifndef PA_WEIGHTS_POLY
+#define PA_WEIGHTS_POLY 2
+#endif
 
 template <int D>
 struct WeightsCfg {
     static constexpr int kTile = D / 64 * kHalfBytes;
-    static constexpr int kStages = 2;
-    static constexpr int kRing = kTile;                       // after the key tile
-    static constexpr int kLse = kRing + kStages * kTile;      // [4 warps][128] floats
-    static constexpr int kExt = kLse + 4 * kBlk * 4;
-    static constexpr int kNumBars = 1 + 2 * kStages + 2 + 2 + 1;  // k, full, empty, s, free, fin
-    static constexpr int kSmem = kExt + 8 * kNumBars + 16;
-    static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
+    static constexpr int kStages = 4;                         // query tiles
+    static constexpr int kRing = 2 * kTile;                   // after two key tiles
+    static constexpr int kLse = kRing + kStages * kTile;      // [warp][128] floats
+    static constexpr int kPart = kLse + kSumWarps * kBlk * 4; // [128] sums of the odd steps
+    static constexpr int kItems = kPart + kBlk * 4;
+    static constexpr int kBars = kItems + kItemBytes;
+    // k 2, its release 2, full S, empty S, s B, its release B, part, its release, fin
+    static constexpr int kNumBars = 4 + 2 * kStages + 2 * kWBufs + 3 + kItemBars;
+    static constexpr int kSmem = kBars + 8 * kNumBars + 8;    // + TMEM slot, dead
+    static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+};
+
+// The queries of an item's key tile: tiles of 128 from the first that counts.
+struct Queries {
+    int key0, first, tiles;
+    __device__ __forceinline__ Queries(const Item& it, int last_queries) {
+        key0 = it.tile * kBlk;
+        first = max(key0, last_queries > 0 ? it.len - last_queries : 0);
+        tiles = (it.len - first + kBlk - 1) / kBlk;
+    }
 };
 
 template <int D>
-__global__ void __launch_bounds__(kWThreads, 2)
+__global__ void __launch_bounds__(kWThreads, 1)
 prefill_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                        const PrefillParams p) {
     using C = WeightsCfg<D>;
@@ -579,160 +850,219 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = p.num_heads / p.num_kv_heads;
-    const int kh = blockIdx.x % p.num_kv_heads;
-    bool bad = false;
-    const PromptTile u = prompt_tile(p, [](int len) { return (len + kBlk - 1) / kBlk; },
-                                     blockIdx.x / p.num_kv_heads, false, &bad);
-    if (bad && kh == 0) atomicOr(&s_status_prefill, kStatusBadIndex);
-    if (u.seq < 0) return;
     const uint32_t raw = smem_u32(smem);
     if (raw & 1023u) {
         if (threadIdx.x == 0) atomicOr(&s_status_prefill, kStatusSmemAlign);
         return;
     }
-    const int key0 = u.tile * kBlk;
-    const int first = p.last_queries > 0 ? max(0, u.len - p.last_queries) : 0;  // first query that counts
-    const int q_tile0 = max(key0, first) / kBlk;
-    const int q_tiles = (u.len + kBlk - 1) / kBlk - q_tile0;
-    const int steps = q_tiles * group;      // (head, query tile), heads outermost
-
-    uint8_t* ext = smem + C::kExt;
-    const uint32_t bars = smem_u32(ext);
-    const uint32_t b_k = bars, b_full = b_k + 8, b_empty = b_full + 8 * S_, b_s = b_empty + 8 * S_,
-                   b_free = b_s + 16, b_fin = b_free + 16;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(ext + 8 * C::kNumBars);
+    const uint32_t bars = smem_u32(smem + C::kBars);
+    const uint32_t b_k = bars, b_kfree = b_k + 16, b_full = b_kfree + 16, b_empty = b_full + 8 * S_,
+                   b_s = b_empty + 8 * S_, b_sfree = b_s + 8 * kWBufs, b_part = b_sfree + 8 * kWBufs,
+                   b_pfree = b_part + 8, b_fin = b_pfree + 8;
+    const ItemBars ib = item_bars(b_fin + 8, smem + C::kItems, kSumWarps + 1);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBars + 8 * C::kNumBars);
     volatile int* dead = reinterpret_cast<volatile int*>(tslot + 1);
     if (threadIdx.x == 0) {
-        mbar_init(b_k, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(b_k + 8 * i, 1);
+            mbar_init(b_kfree + 8 * i, 1);
+        }
         for (int i = 0; i < S_; ++i) {
             mbar_init(b_full + 8 * i, 1);
             mbar_init(b_empty + 8 * i, 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kWBufs; ++i) {
             mbar_init(b_s + 8 * i, 1);
-            mbar_init(b_free + 8 * i, 4);
+            mbar_init(b_sfree + 8 * i, kSumWarps / 2);
         }
+        mbar_init(b_part, kSumWarps / 2);
+        mbar_init(b_pfree, kSumWarps / 2);
         mbar_init(b_fin, 1);
         *dead = 0;
         fence_barrier_init();
     }
-    if (warp == 4) tmem_alloc(smem_u32(tslot), kWTmemCols);
+    if (warp == kSumWarps) tmem_alloc(smem_u32(tslot), kWTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = *tslot;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_or_dead(dead, bar, parity));
+    };
 
-    if (warp < 4) {  // a thread per key
+    if (warp < kSumWarps) {
+        // A thread per key. The two groups of four warps take the steps (head, query tile) in
+        // turn; a key's sum is that of the even steps plus that of the odd ones, whichever
+        // group had them.
+        const int wg = warp >> 2, row = threadIdx.x & 127;
         float* lq = reinterpret_cast<float*>(smem + C::kLse) + warp * kBlk;  // this warp's own
-        const int key = key0 + threadIdx.x;
-        const uint32_t ts = tm + ((uint32_t)(32 * warp) << 16);
+        float* part = reinterpret_cast<float*>(smem + C::kPart) + row;
+        const uint32_t ts = tm + ((uint32_t)(32 * (warp & 3)) << 16);
         const float sl = fabsf(p.scale_log2);
         const float2 sl2 = make_float2(sl, sl);
-        float sum = 0.f;
+        uint32_t done = 0;       // steps of the items before
+        uint32_t par_part = 0;
         bool ok = true;
-        int h = 0, qt = 0;
-        // the log-sum-exps of a step's queries, four to a lane, negated, in log2 units
-        float mine[4];
-        auto fetch = [&](int hh, int tt) {
+        for (int n = 0; ok; ++n) {
+            const Item it = take_item(ib, dead, n);
+            if (it.seq == kEnd) break;
+            if (it.seq < 0) continue;
+            const Queries qs(it, p.last_queries);
+            const int steps = qs.tiles * group;
+            const int key = qs.key0 + row;
+            const int i0 = wg ^ (done & 1);     // this group's first step
+            float sum = 0.f;
+            // the log-sum-exps of a step's queries, four to a lane, negated, in log2 units
+            float mine[4];
+            int h = i0 / qs.tiles, qt = i0 - h * qs.tiles;
+            auto fetch = [&] {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = (q_tile0 + tt) * kBlk + 32 * e + lane;
-                mine[e] = hh < group && i < u.len
-                              ? -kLog2e * __ldg(p.lse + (int64_t)(kh * group + hh) * p.total_tokens + u.start + i)
-                              : 0.f;
+                for (int e = 0; e < 4; ++e) {
+                    const int i = qs.first + qt * kBlk + 32 * e + lane;
+                    mine[e] = h < group && i < it.len
+                                  ? -kLog2e * __ldg(p.lse + (int64_t)(it.kh * group + h) * p.total_tokens +
+                                                    it.start + i)
+                                  : 0.f;
+                }
+            };
+            fetch();
+            for (int i = i0; i < steps; i += 2) {
+                const int q0 = qs.first + qt * kBlk;
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (++qt == qs.tiles) qt = 0, ++h;
+                __syncwarp();  // the previous step's are read
+#pragma unroll
+                for (int e = 0; e < 4; ++e) lq[32 * e + lane] = mine[e];
+                fetch();
+                __syncwarp();
+                const uint32_t g = done + i, buf = g % kWBufs;
+                if (!(ok = wait(b_s + 8 * buf, (g / kWBufs) & 1))) break;
+                tc_fence_after();
+                const bool whole = q0 >= qs.key0 + kBlk && q0 + kBlk <= it.len;
+                const int lo = key - q0, hi = it.len - q0;   // else: the columns that count
+                float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t s[64];
+                    tmem_ld64_issue(ts + kBlk * buf + 64 * half, s);
+                    tmem_wait_ld(s);
+                    if (half == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(b_sfree + 8 * buf);
+                    }
+                    if (whole) {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 4) {
+                            const float4 e = *reinterpret_cast<const float4*>(lq + 64 * half + c);
+                            const float2 x = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sl2,
+                                                  make_float2(e.x, e.y));
+                            const float2 y = fma2(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
+                                                  sl2, make_float2(e.z, e.w));
+                            acc[0] = add2(acc[0], exp2_pair<PA_WEIGHTS_POLY>(x, c / 2));
+                            acc[1] = add2(acc[1], exp2_pair<PA_WEIGHTS_POLY>(y, c / 2 + 1));
+                        }
+                    } else {  // the diagonal, or the prompt's end
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) {
+                            const int col = 64 * half + c;
+                            const float x = ex2(fmaf(__uint_as_float(s[c]), sl, lq[col]));
+                            if (col >= lo && col < hi) acc[c & 1].x += x;
+                        }
+                    }
+                }
+                sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
             }
-        };
-        fetch(0, 0);
-        for (int n = 0; n < steps; ++n) {
-            __syncwarp();  // the previous step's are read
-#pragma unroll
-            for (int e = 0; e < 4; ++e) lq[32 * e + lane] = mine[e];
-            const int q0 = (q_tile0 + qt) * kBlk;
-            if (++qt == q_tiles) {
-                qt = 0;
-                ++h;
-            }
-            fetch(h, qt);
-            __syncwarp();
-            if (!(ok = __all_sync(0xffffffffu, wait_or_dead(dead, b_s + 8 * (n & 1), (n >> 1) & 1)))) break;
-            tc_fence_after();
-            const uint32_t at = ts + 128 * (n & 1);
-            const bool whole = q0 >= key0 + kBlk && q0 >= first && q0 + kBlk <= u.len;
-            const int lo = max(key, first) - q0, hi = u.len - q0;   // columns that count
-            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t s[64];
-                tmem_ld64_issue(at + 64 * half, s);
-                tmem_wait_ld(s);
-                if (half == 1) {  // S^T is in registers
-                    tc_fence_before();
+            if (!ok) break;
+            done += steps;
+            if (steps > 1) {
+                if (i0 == 1) {
+                    if (!(ok = wait(b_pfree, par_part ^ 1))) break;   // (the first wait is for no use yet)
+                    *part = sum;
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(b_free + 8 * (n & 1));
-                }
-                if (whole) {
-#pragma unroll
-                    for (int c = 0; c < 64; c += 4) {
-                        const float4 e = *reinterpret_cast<const float4*>(lq + 64 * half + c);
-                        float2 x = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sl2,
-                                        make_float2(e.x, e.y));
-                        float2 y = fma2(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), sl2,
-                                        make_float2(e.z, e.w));
-                        acc[0] = add2(acc[0], exp2_pair<PA_WEIGHTS_POLY>(x, c / 2));
-                        acc[1] = add2(acc[1], exp2_pair<PA_WEIGHTS_POLY>(y, c / 2 + 1));
-                    }
+                    if (lane == 0) mbar_arrive(b_part);
                 } else {
-#pragma unroll
-                    for (int c = 0; c < 64; ++c) {
-                        const int col = 64 * half + c;
-                        if (col >= lo && col < hi) acc[0].x += ex2(fmaf(__uint_as_float(s[c]), sl, lq[col]));
-                    }
+                    if (!(ok = wait(b_part, par_part))) break;
+                    sum += *part;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(b_pfree);
                 }
+                par_part ^= 1;
             }
-            sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+            if (i0 == 0 && key < it.len)
+                p.weights[((int64_t)it.seq * p.num_kv_heads + it.kh) * p.weights_stride + key] = sum;
         }
-        if (ok && key < u.len)
-            p.weights[((int64_t)u.seq * p.num_kv_heads + kh) * p.weights_stride + key] = sum;
-    } else if (warp == 4) {  // products
+    } else if (warp == kSumWarps) {  // products
         const uint32_t idesc = umma_idesc(kBlk, kBlk, false) | (p.scale_log2 < 0.f ? kNegateA : 0u);
         const bool one = elect_one();
-        const uint32_t k_lo = rows_lo(raw);
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, wait_or_dead(dead, bar, parity));
-        };
-        bool ok = wait(b_k, 0);
-        int st = 0;
-        uint32_t ph = 0;
-        for (int n = 0; n < steps && ok; ++n) {
-            if (n >= 2 && !(ok = wait(b_free + 8 * (n & 1), ((n >> 1) & 1) ^ 1))) break;
-            if (!(ok = wait(b_full + 8 * st, ph))) break;
-            tc_fence_after();
-            const uint32_t d = tm + kBlk * (n & 1), q_lo = rows_lo(raw + C::kRing + st * C::kTile);
-            if (one) {
-                issue_qk<D>(d, k_lo, q_lo, idesc);
-                umma_commit(b_s + 8 * (n & 1));
-                umma_commit(b_empty + 8 * st);
+        Place<2> kt;
+        Place<S_> at;
+        Place<kWBufs> buf;
+        int used = 0;
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            const Item it = take_item(ib, dead, n);
+            if (it.seq == kEnd) break;
+            if (it.seq < 0) continue;
+            const int steps = Queries(it, p.last_queries).tiles * group;
+            if (!(ok = wait(b_k + 8 * kt.st, kt.par))) break;
+            const uint32_t k_lo = rows_lo(raw + kt.st * C::kTile);
+            for (int i = 0; i < steps; ++i, ++used) {
+                if (used >= kWBufs && !(ok = wait(b_sfree + 8 * buf.st, buf.par ^ 1))) break;
+                if (!(ok = wait(b_full + 8 * at.st, at.par))) break;
+                tc_fence_after();
+                const uint32_t d = tm + kBlk * buf.st, q_lo = rows_lo(raw + C::kRing + at.st * C::kTile);
+                if (one) {
+                    issue_qk<D>(d, k_lo, q_lo, idesc);
+                    umma_commit(b_s + 8 * buf.st);
+                    umma_commit(b_empty + 8 * at.st);
+                    if (i == steps - 1) umma_commit(b_kfree + 8 * kt.st);
+                }
+                __syncwarp();
+                at = at.next();
+                buf = buf.next();
             }
-            __syncwarp();
-            if (++st == S_) st = 0, ph ^= 1;
+            kt = kt.next();
         }
         if (one) umma_commit(b_fin);
         __syncwarp();
         if (!mbar_wait_bounded(b_fin, 0)) atomicOr(&s_status_prefill, kStatusTimeout);
-    } else if (lane == 0) {  // loads
-        load_tile<D>(raw, &kmap, kh, u.start + key0, b_k);
-        bool ok = true;
-        int n = 0;
-        for (int h = 0; h < group && ok; ++h) {
-            for (int qt = 0; qt < q_tiles; ++qt, ++n) {
-                if (n >= S_ && !(ok = wait_or_dead(dead, b_empty + 8 * (n % S_), ((n / S_) & 1) ^ 1))) break;
-                load_tile<D>(raw + C::kRing + (n % S_) * C::kTile, &qmap, kh * group + h,
-                             u.start + (q_tile0 + qt) * kBlk, b_full + 8 * (n % S_));
-            }
+    } else {  // loads
+        if (lane == 0) {
+            prefetch_tensormap(&qmap);
+            prefetch_tensormap(&kmap);
         }
-        if (!ok) {  // given up: the loads in flight land before the CTA ends
-            bool landed = mbar_wait_bounded(b_k, 0);
-            for (int i = max(0, n - S_); i < n; ++i)
+        Place<2> kt;
+        Place<S_> at;
+        int keys = 0, loaded = 0;
+        walk_items(
+            p, ib, dead, false, [](int len) { return (len + kBlk - 1) / kBlk; },
+            [&](const Item& it) {
+                bool ok = true;
+                if (lane == 0) {
+                    const Queries qs(it, p.last_queries);
+                    if (keys >= 2) ok = wait_or_dead(dead, b_kfree + 8 * kt.st, kt.par ^ 1);
+                    if (ok) {
+                        load_tile<D>(raw + kt.st * C::kTile, &kmap, it.kh, it.start + qs.key0, b_k + 8 * kt.st);
+                        ++keys;
+                        kt = kt.next();
+                    }
+                    for (int h = 0; h < group && ok; ++h)
+                        for (int qt = 0; qt < qs.tiles; ++qt, ++loaded, at = at.next()) {
+                            if (loaded >= S_ && !(ok = wait_or_dead(dead, b_empty + 8 * at.st, at.par ^ 1))) break;
+                            load_tile<D>(raw + C::kRing + at.st * C::kTile, &qmap, it.kh * group + h,
+                                         it.start + qs.first + qt * kBlk, b_full + 8 * at.st);
+                        }
+                }
+                __syncwarp();
+                return ok;
+            });
+        if (lane == 0 && *dead != 0) {  // given up: the loads in flight land before the CTA ends
+            bool landed = true;
+            for (int i = max(0, keys - 2); i < keys; ++i)
+                landed &= mbar_wait_bounded(b_k + 8 * (i & 1), (i >> 1) & 1);
+            for (int i = max(0, loaded - S_); i < loaded; ++i)
                 landed &= mbar_wait_bounded(b_full + 8 * (i % S_), (i / S_) & 1);
             if (!landed) atomicOr(&s_status_prefill, kStatusTimeout);
         }
@@ -741,7 +1071,7 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 4) tmem_dealloc(tm, kWTmemCols);
+    if (warp == kSumWarps) tmem_dealloc(tm, kWTmemCols);
 }
 
 template <int D>

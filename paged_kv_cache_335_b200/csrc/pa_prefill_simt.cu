@@ -73,11 +73,11 @@ prefill_simt_kernel(const PrefillParams p) {
     float* qt = sm;                  // [D][kPad]
     float* kt = qt + D * kPad;       // [D][kPad]; then the weights [key][kPad]
     float* vs = kt + D * kPad;       // [kB][D]
-    bool bad = false;
     const auto tiles = [](int len) { return (len + kB - 1) / kB; };
-    const PromptTile t = prompt_tile(p, tiles, blockIdx.x, true, &bad);
+    PromptWalk walk;
+    const PromptTile t = walk.find(p, tiles, blockIdx.x, true);
     const int h = blockIdx.y;
-    if (bad && h == 0) atomicOr(&s_status_prefill_simt, kStatusBadIndex);
+    if (walk.bad && h == 0) atomicOr(&s_status_prefill_simt, kStatusBadIndex);
     if (t.seq < 0) return;
     const int kh = h / (p.num_heads / p.num_kv_heads);
     const float* q = static_cast<const float*>(p.q) + (int64_t)h * D;
@@ -183,11 +183,11 @@ prefill_weights_simt_kernel(const PrefillParams p) {
     float* kt = sm;                  // [D][kPad]
     float* qt = kt + D * kPad;
     float* lq = qt + D * kPad;       // [kB] log-sum-exp of the queries, log2 units
-    bool bad = false;
     const auto tiles = [](int len) { return (len + kB - 1) / kB; };
-    const PromptTile t = prompt_tile(p, tiles, blockIdx.x, false, &bad);
+    PromptWalk walk;
+    const PromptTile t = walk.find(p, tiles, blockIdx.x, false);
     const int kh = blockIdx.y;
-    if (bad && kh == 0) atomicOr(&s_status_prefill_simt, kStatusBadIndex);
+    if (walk.bad && kh == 0) atomicOr(&s_status_prefill_simt, kStatusBadIndex);
     if (t.seq < 0) return;
     const int group = p.num_heads / p.num_kv_heads;
     const float* k = static_cast<const float*>(p.k) + (int64_t)kh * D;

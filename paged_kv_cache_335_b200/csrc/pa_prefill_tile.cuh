@@ -15,53 +15,71 @@ struct PromptTile {
     int tile;   // which of the prompt's tiles
 };
 
-// Tile `u` of the packed prompts, found by a whole warp from the sequence starts (32
-// prompts per step): prompts in order, each with tiles(its length) tiles, counted from
-// the last to the first when `reversed`. A prompt with bad bounds (outside
-// [0, total_tokens], negative length, or longer than max_seq_len) has no tile; *bad
-// reports it.
-template <typename Tiles>
-__device__ __forceinline__ PromptTile prompt_tile(const PrefillParams& p, Tiles tiles, int u,
-                                                  bool reversed, bool* bad) {
-    const int lane = threadIdx.x & 31;
-    PromptTile r;
-    r.seq = -1;
-    int seen = 0;
-    for (int base = 0; base < p.num_seqs; base += 32) {
+// Finds tiles of the packed prompts by their index, a whole warp at a time: prompts in
+// order, each with tiles(its length) tiles, counted from the last to the first when
+// `reversed`. A prompt with bad bounds (outside [0, total_tokens], negative
+// length, or longer than max_seq_len) has no tile; `bad` reports that the lane met one.
+// The warp holds 32 prompts (one per lane) and the number of tiles before them; an index at
+// or behind those goes on from there, so indices that ascend read each prompt once.
+struct PromptWalk {
+    int base = 0;      // prompts of the lanes: base ..
+    int seen = 0;      // tiles before them
+    int start = 0, len = 0, count = 0, before = 0;   // the lane's prompt, its tiles, tiles before it
+    int total = 0;     // tiles of the 32
+    bool loaded = false, bad = false;
+
+    template <typename Tiles>
+    __device__ __forceinline__ void load(const PrefillParams& p, Tiles tiles) {
+        const int lane = threadIdx.x & 31;
         const int s = base + lane;
-        int a = 0, len = 0;
+        start = len = 0;
         if (s < p.num_seqs) {
-            a = __ldg(p.cu_seqlens + s);
+            start = __ldg(p.cu_seqlens + s);
             const int b = __ldg(p.cu_seqlens + s + 1);
-            len = b - a;
-            if (a < 0 || b < a || b > p.total_tokens || len > p.max_seq_len) {
-                *bad = true;
+            len = b - start;
+            if (start < 0 || b < start || b > p.total_tokens || len > p.max_seq_len) {
+                bad = true;
                 len = 0;
             }
         }
-        const int nt = tiles(len);
-        int x = nt;
+        count = tiles(len);
+        int x = count;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, x, off);
             if (lane >= off) x += y;
         }
-        const int mine = seen + x - nt;  // tiles before this lane's prompt
-        const bool hit = u >= mine && u < mine + nt;
-        const uint32_t hits = __ballot_sync(0xffffffffu, hit);
-        if (hits) {
-            const int l = __ffs(hits) - 1;
-            const int t = u - __shfl_sync(0xffffffffu, mine, l);
-            const int n = __shfl_sync(0xffffffffu, nt, l);
-            r.seq = base + l;
-            r.start = __shfl_sync(0xffffffffu, a, l);
-            r.len = __shfl_sync(0xffffffffu, len, l);
-            r.tile = reversed ? n - 1 - t : t;
-            return r;
-        }
-        seen += __shfl_sync(0xffffffffu, x, 31);
+        before = seen + x - count;
+        total = __shfl_sync(0xffffffffu, x, 31);
+        loaded = true;
     }
-    return r;
-}
+
+    template <typename Tiles>
+    __device__ __forceinline__ PromptTile find(const PrefillParams& p, Tiles tiles, int u, bool reversed) {
+        PromptTile r;
+        r.seq = -1;
+        r.start = r.len = r.tile = 0;
+        if (u < seen) {  // behind an index that came before: from the start again
+            base = seen = 0;
+            loaded = false;
+        }
+        if (!loaded) load(p, tiles);
+        while (u >= seen + total) {
+            if (base + 32 >= p.num_seqs) return r;
+            base += 32;
+            seen += total;
+            load(p, tiles);
+        }
+        const uint32_t hits = __ballot_sync(0xffffffffu, u >= before && u < before + count);
+        const int l = __ffs(hits) - 1;
+        const int t = u - __shfl_sync(0xffffffffu, before, l);
+        const int n = __shfl_sync(0xffffffffu, count, l);
+        r.seq = base + l;
+        r.start = __shfl_sync(0xffffffffu, start, l);
+        r.len = __shfl_sync(0xffffffffu, len, l);
+        r.tile = reversed ? n - 1 - t : t;
+        return r;
+    }
+};
 
 }  // namespace pa
