@@ -16,7 +16,10 @@
 //   warp 17: loads Q and the ring of K and V tiles by TMA, and finds the next item;
 //   warps 0..7 and 8..15: the softmax of row blocks 0 and 1, two threads per row (of warps
 //     that share TMEM lanes), which exchange the row's maximum in every tile and its sum at
-//     the end. P (bf16) overwrites the first half of its S in TMEM;
+//     the end. P (bf16) overwrites the first half of each thread's scores in TMEM, which are
+//     read twice (for the maximum, then for the weights): kept in registers, they
+//     left the rest of the loop to local memory, and with shared memory taking all of
+//     the L1 cache each of those loads is an L2 access;
 //   warps 18 and 19: on the tiles that the diagonal crosses, zero the elements of V that are
 //     not finite, and the rows behind the prompt, before the tensor core reads
 //     them: a masked weight is 0, and 0 x infinity would not be. The epilogue adds the
@@ -366,27 +369,14 @@ __device__ __forceinline__ bool pair_any(int id, bool pred) {
     return r != 0;
 }
 
-// The weights 2^(s sl - ms) of half a row: bf16 into TMEM at ts; returns their fp32 sum in
-// two parts.
-__device__ __forceinline__ float2 put_weights(const uint32_t (&s)[64], float sl, float ms, uint32_t ts) {
-    const float2 sl2 = make_float2(sl, sl), ms2 = make_float2(-ms, -ms);
-    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+// 32 scores of a row from TMEM; on the diagonal's tile those past column `lim` are masked.
+__device__ __forceinline__ void load_scores(uint32_t at, bool diagonal, int lim, uint32_t (&s)[32]) {
+    tmem_ld32(at, s);
+    if (diagonal) {
 #pragma unroll
-    for (int g = 0; g < 64; g += 32) {
-        uint32_t w[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-            const int at = g + 2 * c;
-            float2 x = fma2(make_float2(__uint_as_float(s[at]), __uint_as_float(s[at + 1])), sl2, ms2);
-            x.x = ex2(x.x);
-            x.y = ex2(x.y);
-            w[c] = bf16x2(x.x, x.y);
-            sum[c & 1] = add2(sum[c & 1], x);
-        }
-        tmem_st16_issue(ts + g / 2, w);
+        for (int c = 0; c < 32; ++c)
+            if (c > lim) s[c] = 0xff800000u;
     }
-    tmem_wait_st();
-    return add2(sum[0], sum[1]);
 }
 
 template <int D>
@@ -441,16 +431,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         return __all_sync(0xffffffffu, wait_or_dead(dead, bar, parity));
     };
 
-    // 640 threads get 96 registers each: the 512 of the softmax take 104, the others 64
-    if (warp < kSoftWarps)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    else
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp < kSoftWarps) {  // softmax of row block b: half a row per thread
         const int b = warp >> 3, half = (warp >> 2) & 1, row = threadIdx.x & 127;
         const int pair_id = 1 + 4 * b + (warp & 3);
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t ts = tm + lanes + kBlk * b, to = tm + lanes + C::kColO + D * b + D / 2 * half;
+        const uint32_t ts = tm + lanes + kBlk * b + 64 * half, to = tm + lanes + C::kColO + D * b + D / 2 * half;
         float* xch = reinterpret_cast<float*>(smem + C::kXch) + 2 * kBlk * b + row;
         // (its sign is in the product; not 0, so that a masked -infinity stays one)
         const float sl = fmaxf(fabsf(p.scale_log2), 1e-30f);
@@ -471,30 +456,27 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             float2 l2 = make_float2(0.f, 0.f);
             for (int j = 0; j <= last; ++j, par_s ^= 1) {
                 ok = wait(b_s + 8 * b, par_s);
-                uint32_t s[64];
+                const bool diagonal = j == last;
                 float mt = -INFINITY;
                 if (ok) {
                     tc_fence_after();
-                    tmem_ld64_issue(ts + 64 * half, s);
-                    tmem_wait_ld(s);
-                    if (j == last) {  // the tile the diagonal crosses
-                        const int lim = row - 64 * half;
-#pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            if (c > lim) s[c] = 0xff800000u;
-                    }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int c = 0; c < 64; c += 8)
+                    for (int g = 0; g < 2; ++g) {
+                        uint32_t s[32];
+                        load_scores(ts + 32 * g, diagonal, row - 64 * half - 32 * g, s);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(s[c + i])), __uint_as_float(s[c + 4 + i]));
+                        for (int c = 0; c < 32; c += 8)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(s[c + i])), __uint_as_float(s[c + 4 + i]));
+                    }
                     mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     // (the other thread has read the last one: it did so before its weights,
                     // which S_b's product waited for)
                     xch[half * kBlk] = mt;
                 }
-                // both halves are in registers (P may overwrite S) and their maxima known
+                // both halves' maxima are known
                 if (pair_any(pair_id, !ok)) {
                     ok = false;
                     break;
@@ -524,7 +506,25 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                         }
                     }
                 }
-                l2 = add2(l2, put_weights(s, sl, ms, ts + 32 * half));
+                // the weights 2^(s sl - ms), bf16, over the first half of this thread's scores
+                const float2 sl2 = make_float2(sl, sl), ms2 = make_float2(-ms, -ms);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t s[32], w[16];
+                    load_scores(ts + 32 * g, diagonal, row - 64 * half - 32 * g, s);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        float2 x = fma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sl2, ms2);
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
+                        w[c] = bf16x2(x.x, x.y);
+                        sum[c & 1] = add2(sum[c & 1], x);
+                    }
+                    tmem_st16_issue(ts + 16 * g, w);
+                }
+                tmem_wait_st();
+                l2 = add2(l2, add2(sum[0], sum[1]));
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_p + 8 * b);
@@ -656,8 +656,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                     if (one) {
 #pragma unroll
                         for (int i = 0; i < kBlk / 16; ++i)
-                            umma_ts_words(tm + C::kColO + D * b, tm + kBlk * b + 8 * i, lo + 128 * i, kDescHi,
-                                          C::kIdescPV, i > 0 || j > 0);
+                            umma_ts_words(tm + C::kColO + D * b, tm + kBlk * b + 8 * i + (i < 4 ? 0 : 32), lo + 128 * i,
+                                          kDescHi, C::kIdescPV, i > 0 || j > 0);
                         if (last) {
                             umma_commit(b_o + 8 * b);
                             noted[b] = note;
@@ -693,7 +693,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         }
         Place<S_> at;
         int loaded = 0;                    // tiles of the ring
-        int used_q[2] = {0, 0}, edges = 0, edge_at[2] = {0, 0};
+        int used_q[2] = {0, 0}, edges = 0, edge1 = 0, edge2 = 0;   // the last two edge tiles' places
         walk_items(
             p, ib, dead, true, [group](int len) { return ((len + kBlk - 1) / kBlk * group + 1) / 2; },
             [&](const Item& it) {
@@ -716,16 +716,16 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                         if (edge) {
                             // the tile that used this edge slot before has been released, so
                             // nobody still waits for that use's phases
-                            const int before = edge_at[edges & 1];
-                            if (edges >= 2 && before + S_ > loaded &&
-                                !(ok = wait_or_dead(dead, b_empty + 8 * (before % S_), (before / S_) & 1)))
+                            if (edges >= 2 && edge2 + S_ > loaded &&
+                                !(ok = wait_or_dead(dead, b_empty + 8 * (edge2 % S_), (edge2 / S_) & 1)))
                                 break;
                         }
                         load_tile<D>(ring + at.st * C::kTile, i & 1 ? &vmap : &kmap, it.kh, it.start + j * kBlk,
                                      b_full + 8 * at.st);
                         if (edge) {
                             mbar_arrive(b_edge + 8 * (edges & 1));
-                            edge_at[edges & 1] = loaded;
+                            edge2 = edge1;
+                            edge1 = loaded;
                             ++edges;
                         }
                         if (i == 0 && k.nb == 2) ok = load_q(1);
