@@ -101,6 +101,13 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 __device__ __forceinline__ float2 sub2(float2 a, float2 b) {
     return fma2(b, make_float2(-1.f, -1.f), a);
 }
@@ -113,11 +120,11 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 // 2^x of two values, x <= 128, on the fp32 units instead of the exponential unit: with n =
 // round(x) (by adding 1.5 x 2^23) and f = x - n in [-1/2, 1/2], 2^f by its degree-5
 // polynomial of least relative error (Remez exchange; below 2.4e-7 in fp32 arithmetic),
-// and n added to the exponent bits. x <= -127 gives 0.
+// times 2^n made of its exponent bits. x <= -127 gives 0, NaN stays NaN.
 __device__ __forceinline__ float2 exp2_poly(float2 x) {
     const float2 big = make_float2(12582912.f, 12582912.f);
-    x.x = fmaxf(x.x, -127.f);
-    x.y = fmaxf(x.y, -127.f);
+    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.x));  // -127
+    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.y));
     const float2 t = add2(x, big);
     const float2 f = add2(x, sub2(big, t));
     auto both = [](float c) { return make_float2(c, c); };
@@ -126,8 +133,8 @@ __device__ __forceinline__ float2 exp2_poly(float2 x) {
     y = fma2(f, y, both(0.24022120237350464f));
     y = fma2(f, y, both(0.6931469440460205f));
     y = fma2(f, y, both(1.0000001192092896f));
-    return make_float2(__int_as_float(__float_as_int(y.x) + (__float_as_int(t.x) << 23)),
-                       __int_as_float(__float_as_int(y.y) + (__float_as_int(t.y) << 23)));
+    return mul2(y, make_float2(__int_as_float((__float_as_int(t.x) << 23) + 0x3f800000),
+                               __int_as_float((__float_as_int(t.y) << 23) + 0x3f800000)));
 }
 
 // 2^x of the pair with index c of a row: kPoly of every eight pairs by polynomial, the
@@ -176,7 +183,7 @@ __device__ __forceinline__ void issue_qk(uint32_t d, uint32_t a, uint32_t b, uin
 // ---------------------------------------------------------------------------
 // items
 // ---------------------------------------------------------------------------
-// What a CTA works on next: one (prompt, kv head, tile), decoded by the loading warp.
+// What a CTA works on next: one (prompt, kv head, tile), decoded by one of its warps.
 struct Item {
     int seq;    // kNothing: the index lies behind the last one; kEnd: no more
     int start, len, tile, kh;
@@ -209,8 +216,8 @@ __device__ __forceinline__ int answer_index(uint32_t response) {
     return yes ? (int)x : -1;
 }
 
-// The loading warp: hands over the item with index `id`, loads it by load(item) (false: gave
-// up), and goes on with the next.
+// One warp: hands over the CTA's first item, calls load(item) (false: gave up), and goes on
+// with the next.
 template <typename Tiles, typename Load>
 __device__ __forceinline__ void walk_items(const PrefillParams& p, const ItemBars& ib, volatile int* dead,
                                            bool reversed, Tiles tiles, Load load) {
@@ -324,6 +331,12 @@ struct Place {
 // ---------------------------------------------------------------------------
 // attention
 // ---------------------------------------------------------------------------
+#ifndef PA_ATTN_POLY
+#define PA_ATTN_POLY 1
+#endif
+#ifndef PA_ATTN_POLY64
+#define PA_ATTN_POLY64 1
+#endif
 constexpr int kCleaners = 2;              // warps
 constexpr int kSoftWarps = 16;            // eight per row block, then products, loads, cleaners
 constexpr int kAttnThreads = 32 * (kSoftWarps + 2 + kCleaners);
@@ -342,6 +355,7 @@ struct AttnCfg {
     static constexpr int kNumBars = 2 * kStages + 17 + kItemBars;
     static constexpr int kSmem = kBars + 8 * kNumBars + 32;   // + TMEM slot, dead, taken 4, noted 2
     static constexpr uint32_t kColO = 256;
+    static constexpr int kPoly = D == 64 ? PA_ATTN_POLY64 : PA_ATTN_POLY;   // see exp2_pair
     static constexpr uint32_t kIdescQK = umma_idesc(kBlk, kBlk, false);
     static constexpr uint32_t kIdescPV = umma_idesc(kBlk, D, true);
     static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
@@ -484,7 +498,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 mt = fmaxf(mt, xch[(half ^ 1) * kBlk]);
                 if (j == 0) {
                     m = mt;
-                    ms = m * sl;
+                    ms = m == -INFINITY ? 0.f : m * sl;   // (no score above -infinity yet: weights 0)
                 } else {
                     const bool move = (mt - m) * sl > kRescaleLog2;
                     if (__any_sync(0xffffffffu, move)) {
@@ -516,8 +530,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
                         float2 x = fma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sl2, ms2);
-                        x.x = ex2(x.x);
-                        x.y = ex2(x.y);
+                        x = exp2_pair<C::kPoly>(x, c);
                         w[c] = bf16x2(x.x, x.y);
                         sum[c & 1] = add2(sum[c & 1], x);
                     }
@@ -808,8 +821,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
 // ---------------------------------------------------------------------------
 // weights
 // ---------------------------------------------------------------------------
-constexpr int kSumWarps = 8;              // two groups of four, then products, loads
-constexpr int kWThreads = 32 * (kSumWarps + 2);
+constexpr int kSumWarps = 8;              // two groups of four, then products, loads, items
+constexpr int kWThreads = 32 * (kSumWarps + 3);
 constexpr int kWBufs = 4;                 // of S^T
 constexpr uint32_t kWTmemCols = kWBufs * kBlk;
 #ifndef PA_WEIGHTS_POLY
@@ -859,7 +872,7 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
     const uint32_t b_k = bars, b_kfree = b_k + 16, b_full = b_kfree + 16, b_empty = b_full + 8 * S_,
                    b_s = b_empty + 8 * S_, b_sfree = b_s + 8 * kWBufs, b_part = b_sfree + 8 * kWBufs,
                    b_pfree = b_part + 8, b_fin = b_pfree + 8;
-    const ItemBars ib = item_bars(b_fin + 8, smem + C::kItems, kSumWarps + 1);
+    const ItemBars ib = item_bars(b_fin + 8, smem + C::kItems, kSumWarps + 2);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBars + 8 * C::kNumBars);
     volatile int* dead = reinterpret_cast<volatile int*>(tslot + 1);
     if (threadIdx.x == 0) {
@@ -1028,7 +1041,7 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
         if (one) umma_commit(b_fin);
         __syncwarp();
         if (!mbar_wait_bounded(b_fin, 0)) atomicOr(&s_status_prefill, kStatusTimeout);
-    } else {  // loads
+    } else if (warp == kSumWarps + 1) {  // loads
         if (lane == 0) {
             prefetch_tensormap(&qmap);
             prefetch_tensormap(&kmap);
@@ -1036,28 +1049,26 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
         Place<2> kt;
         Place<S_> at;
         int keys = 0, loaded = 0;
-        walk_items(
-            p, ib, dead, false, [](int len) { return (len + kBlk - 1) / kBlk; },
-            [&](const Item& it) {
-                bool ok = true;
-                if (lane == 0) {
-                    const Queries qs(it, p.last_queries);
-                    if (keys >= 2) ok = wait_or_dead(dead, b_kfree + 8 * kt.st, kt.par ^ 1);
-                    if (ok) {
-                        load_tile<D>(raw + kt.st * C::kTile, &kmap, it.kh, it.start + qs.key0, b_k + 8 * kt.st);
-                        ++keys;
-                        kt = kt.next();
-                    }
-                    for (int h = 0; h < group && ok; ++h)
-                        for (int qt = 0; qt < qs.tiles; ++qt, ++loaded, at = at.next()) {
-                            if (loaded >= S_ && !(ok = wait_or_dead(dead, b_empty + 8 * at.st, at.par ^ 1))) break;
-                            load_tile<D>(raw + C::kRing + at.st * C::kTile, &qmap, it.kh * group + h,
-                                         it.start + qs.first + qt * kBlk, b_full + 8 * at.st);
-                        }
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            const Item it = take_item(ib, dead, n);
+            if (it.seq == kEnd) break;
+            if (it.seq < 0) continue;
+            const Queries qs(it, p.last_queries);
+            if (keys >= 2 && !(ok = wait(b_kfree + 8 * kt.st, kt.par ^ 1))) break;
+            if (lane == 0)
+                load_tile<D>(raw + kt.st * C::kTile, &kmap, it.kh, it.start + qs.key0, b_k + 8 * kt.st);
+            ++keys;
+            kt = kt.next();
+            for (int h = 0; h < group && ok; ++h)
+                for (int qt = 0; qt < qs.tiles; ++qt, ++loaded, at = at.next()) {
+                    if (loaded >= S_ && !(ok = wait(b_empty + 8 * at.st, at.par ^ 1))) break;
+                    if (lane == 0)
+                        load_tile<D>(raw + C::kRing + at.st * C::kTile, &qmap, it.kh * group + h,
+                                     it.start + qs.first + qt * kBlk, b_full + 8 * at.st);
+                    __syncwarp();
                 }
-                __syncwarp();
-                return ok;
-            });
+        }
         if (lane == 0 && *dead != 0) {  // given up: the loads in flight land before the CTA ends
             bool landed = true;
             for (int i = max(0, keys - 2); i < keys; ++i)
@@ -1066,6 +1077,9 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
                 landed &= mbar_wait_bounded(b_full + 8 * (i % S_), (i / S_) & 1);
             if (!landed) atomicOr(&s_status_prefill, kStatusTimeout);
         }
+    } else {  // items
+        walk_items(p, ib, dead, false, [](int len) { return (len + kBlk - 1) / kBlk; },
+                   [](const Item&) { return true; });
     }
     __syncwarp();
     tc_fence_before();

@@ -118,9 +118,10 @@ prefill_simt_kernel(const PrefillParams p) {
             }
 #pragma unroll
             for (int off = 1; off < 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            const float mn = fmaxf(m[i], mx);
-            const float al = exp2f(m[i] - mn);
-            m[i] = mn;
+            const float old = m[i];
+            m[i] = fmaxf(old, mx);
+            const float mn = m[i] == -INFINITY ? 0.f : m[i];  // (no score above -infinity yet: weights 0)
+            const float al = exp2f(old - mn);
             float sum = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {

@@ -129,6 +129,26 @@ def test_masked_rows_hold_anything(dtype, value, at):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+def test_scores_of_minus_infinity(dtype):
+    """Keys whose scores are -infinity have no weight, also where they fill the first tiles; a row
+    of nothing else has an lse of -infinity."""
+    lens, h, hkv, d = [300], 2, 1, 64
+    q, k, v, cu, cut = _inputs(lens, h, hkv, d, dtype, seed=16, packed=False)
+    q.abs_().add_(0.1)
+    dead = list(range(0, 140)) + [200]
+    k[dead] = float("-inf")
+    out, lse = torch.empty_like(q), torch.empty((h, 300), device=DEV)
+    pa.pa_prefill(out, q, k, v, cut, 0.125, lse=lse)
+    pa.pa_sync_check()
+    assert bool((lse[:, :140] == -math.inf).all())
+    live = [i for i in range(300) if i not in dead]
+    ref, rl, mag, sabs = P.prompt_attention(q[live], k[live], v[live], 0.125)
+    tol = P.attention_bound(ref, mag, sabs, d, 300, dtype)
+    assert bool(((out[live].double() - ref).abs() <= tol).all())
+    assert bool(((lse[:, live].double() - rl).abs() <= P.lse_bound(rl, sabs, d, 300)).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_prompts_do_not_depend_on_the_batch(dtype):
     lens, h, hkv, d = [129, 300, 64, 513], 8, 2, 64
     q, k, v, cu, cut = _inputs(lens, h, hkv, d, dtype, seed=10, packed=False)
@@ -218,6 +238,11 @@ def test_weights_take_no_part_of_later_tokens(dtype, value):
     pa.pa_prefill_weights(w2, bad, k, lse, cut, 0.125)
     pa.pa_sync_check()
     assert torch.equal(w2[0, :, 151:], w[0, :, 151:]) and torch.equal(w2[1], w[1])
+    for i in (128, 129, 150, 151, 152, 153, 154, 155):            # and it is in the earlier keys' weights
+        lse2 = lse.clone()
+        lse2[:, i] = float("nan")
+        pa.pa_prefill_weights(w2, q, k, lse2, cut, 0.125)
+        assert bool(torch.isnan(w2[0, :, :i + 1]).all()) and torch.equal(w2[0, :, i + 1:], w[0, :, i + 1:])
 
 
 def test_negative_scale_weights():
