@@ -132,6 +132,7 @@ struct PrefillParams {
     int64_t weights_stride;
     int32_t num_seqs, total_tokens, max_seq_len, num_heads, num_kv_heads, head_dim;
     int32_t last_queries;       // pa_prefill_weights: 0 = every query
+    int32_t split_heads;        // pa_prefill_weights, set by its launcher
     float scale_log2;           // softmax scale * log2(e)
 };
 

@@ -32,7 +32,9 @@
 //
 // Weights. weights[t] = sum over heads of the group and queries i >= t of
 // 2^(score - lse_i): S^T = K Q^T with the keys as rows, so that a key's sum stays in one
-// thread (two: query tiles in turn); query tiles stream past one key tile. A part of the exponentials runs on the fp32 units.
+// thread (two: one per half of the queries' columns); query tiles stream past two key tiles (one would read each from L2 twice as
+// often, which bounded it: 0.77 us per 128 x 128 scores and SM). A part of the
+// exponentials runs on the fp32 units.
 //
 // Both kernels stay on their SM and take item after item: the grid is one CTA per item, and a
 // running CTA cancels the launch of one that has not started and does its work
@@ -44,6 +46,8 @@
 // 128 x 128 weights) and, in between, by the chain S -> softmax -> P V -> next S of a row
 // block, which the other row block only partly covers.
 #include <math.h>
+
+#include <algorithm>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -137,11 +141,11 @@ __device__ __forceinline__ float2 exp2_poly(float2 x) {
                                __int_as_float((__float_as_int(t.y) << 23) + 0x3f800000)));
 }
 
-// 2^x of the pair with index c of a row: kPoly of every eight pairs by polynomial, the
-// others by the exponential unit, which alone would bound the kernel.
-template <int kPoly>
+// 2^x of the pair with index c of a row: one of every eight pairs by polynomial, the others
+// by the exponential unit (none, 1, 2 and 3 of eight measured: 8K weights 703, 661, 664
+// and 688 us, ragged prompts of head_dim 64 122, 117, 117 and 118 us).
 __device__ __forceinline__ float2 exp2_pair(float2 x, int c) {
-    if ((c & 7) * kPoly % 8 + kPoly > 7) return exp2_poly(x);  // spread evenly (compile time)
+    if (c % 8 == 7) return exp2_poly(x);  // (compile time)
     return make_float2(ex2(x.x), ex2(x.y));
 }
 
@@ -216,10 +220,10 @@ __device__ __forceinline__ int answer_index(uint32_t response) {
     return yes ? (int)x : -1;
 }
 
-// One warp: hands over the CTA's first item, calls load(item) (false: gave up), and goes on
+// One warp: hands over the CTA's first item (index = tile * heads + kv head), calls load(item) (false: gave up), and goes on
 // with the next.
 template <typename Tiles, typename Load>
-__device__ __forceinline__ void walk_items(const PrefillParams& p, const ItemBars& ib, volatile int* dead,
+__device__ __forceinline__ void walk_items(const PrefillParams& p, int heads, const ItemBars& ib, volatile int* dead,
                                            bool reversed, Tiles tiles, Load load) {
     const int lane = threadIdx.x & 31;
     int id = blockIdx.x;
@@ -228,8 +232,8 @@ __device__ __forceinline__ void walk_items(const PrefillParams& p, const ItemBar
         Item it;
         it.seq = kEnd;
         if (id >= 0) {
-            it.kh = id % p.num_kv_heads;
-            const PromptTile u = walk.find(p, tiles, id / p.num_kv_heads, reversed);
+            it.kh = id % heads;
+            const PromptTile u = walk.find(p, tiles, id / heads, reversed);
             it.seq = u.seq;
             it.start = u.start;
             it.len = u.len;
@@ -331,12 +335,6 @@ struct Place {
 // ---------------------------------------------------------------------------
 // attention
 // ---------------------------------------------------------------------------
-#ifndef PA_ATTN_POLY
-#define PA_ATTN_POLY 1
-#endif
-#ifndef PA_ATTN_POLY64
-#define PA_ATTN_POLY64 1
-#endif
 constexpr int kCleaners = 2;              // warps
 constexpr int kSoftWarps = 16;            // eight per row block, then products, loads, cleaners
 constexpr int kAttnThreads = 32 * (kSoftWarps + 2 + kCleaners);
@@ -355,7 +353,6 @@ struct AttnCfg {
     static constexpr int kNumBars = 2 * kStages + 17 + kItemBars;
     static constexpr int kSmem = kBars + 8 * kNumBars + 32;   // + TMEM slot, dead, taken 4, noted 2
     static constexpr uint32_t kColO = 256;
-    static constexpr int kPoly = D == 64 ? PA_ATTN_POLY64 : PA_ATTN_POLY;   // see exp2_pair
     static constexpr uint32_t kIdescQK = umma_idesc(kBlk, kBlk, false);
     static constexpr uint32_t kIdescPV = umma_idesc(kBlk, D, true);
     static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
@@ -530,7 +527,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
                         float2 x = fma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sl2, ms2);
-                        x = exp2_pair<C::kPoly>(x, c);
+                        x = exp2_pair(x, c);
                         w[c] = bf16x2(x.x, x.y);
                         sum[c & 1] = add2(sum[c & 1], x);
                     }
@@ -708,7 +705,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         int loaded = 0;                    // tiles of the ring
         int used_q[2] = {0, 0}, edges = 0, edge1 = 0, edge2 = 0;   // the last two edge tiles' places
         walk_items(
-            p, ib, dead, true, [group](int len) { return ((len + kBlk - 1) / kBlk * group + 1) / 2; },
+            p, p.num_kv_heads, ib, dead, true, [group](int len) { return ((len + kBlk - 1) / kBlk * group + 1) / 2; },
             [&](const Item& it) {
                 bool ok = true;
                 if (lane == 0) {
@@ -821,36 +818,52 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
 // ---------------------------------------------------------------------------
 // weights
 // ---------------------------------------------------------------------------
-constexpr int kSumWarps = 8;              // two groups of four, then products, loads, items
+constexpr int kSumWarps = 16;             // eight per key tile, then products, loads, items
 constexpr int kWThreads = 32 * (kSumWarps + 3);
-constexpr int kWBufs = 4;                 // of S^T
-constexpr uint32_t kWTmemCols = kWBufs * kBlk;
-#ifndef PA_WEIGHTS_POLY
-#define PA_WEIGHTS_POLY 2
-#endif
+constexpr uint32_t kWTmemCols = 512;      // S^T of two key tiles, two buffers each
 
 template <int D>
 struct WeightsCfg {
     static constexpr int kTile = D / 64 * kHalfBytes;
-    static constexpr int kStages = 4;                         // query tiles
-    static constexpr int kRing = 2 * kTile;                   // after two key tiles
-    static constexpr int kLse = kRing + kStages * kTile;      // [warp][128] floats
-    static constexpr int kPart = kLse + kSumWarps * kBlk * 4; // [128] sums of the odd steps
-    static constexpr int kItems = kPart + kBlk * 4;
+    static constexpr int kStages = 3;                         // query tiles with their log-sum-exps
+    static constexpr int kRing = 4 * kTile;                   // after two pairs of key tiles
+    static constexpr int kLse = kRing + kStages * kTile;      // [stage][128] floats
+    static constexpr int kXch = kLse + kStages * kBlk * 4;    // [2 key tiles][128] sums of a half
+    static constexpr int kItems = kXch + 2 * kBlk * 4;
     static constexpr int kBars = kItems + kItemBytes;
-    // k 2, its release 2, full S, empty S, s B, its release B, part, its release, fin
-    static constexpr int kNumBars = 4 + 2 * kStages + 2 * kWBufs + 3 + kItemBars;
+    // k 2, its release 2, full S, empty S, s 2 x 2, its release 2 x 2, fin
+    static constexpr int kNumBars = 4 + 2 * kStages + 8 + 1 + kItemBars;
     static constexpr int kSmem = kBars + 8 * kNumBars + 8;    // + TMEM slot, dead
     static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
-// The queries of an item's key tile: tiles of 128 from the first that counts.
+// An item's queries: tiles of 128 from the first that counts for its first key tile.
 struct Queries {
-    int key0, first, tiles;
+    int len, key0, first, tiles;
     __device__ __forceinline__ Queries(const Item& it, int last_queries) {
-        key0 = it.tile * kBlk;
-        first = max(key0, last_queries > 0 ? it.len - last_queries : 0);
-        tiles = (it.len - first + kBlk - 1) / kBlk;
+        len = it.len;
+        key0 = 2 * it.tile * kBlk;
+        first = max(key0, last_queries > 0 ? len - last_queries : 0);
+        tiles = (len - first + kBlk - 1) / kBlk;
+    }
+    __device__ __forceinline__ int q0(int qt) const { return first + qt * kBlk; }
+    __device__ __forceinline__ bool exists(int w) const { return key0 + w * kBlk < len; }
+    // whether any query of tile qt sees a key of key tile w
+    __device__ __forceinline__ bool meets(int w, int qt) const {
+        return exists(w) && q0(qt) + kBlk > key0 + w * kBlk;
+    }
+};
+
+// The heads of the group that an item takes: all, or (item kv heads 2 kh and 2 kh + 1) a half.
+struct Heads {
+    int first, last;
+    bool split;
+    __device__ __forceinline__ Heads(Item& it, const PrefillParams& p) {
+        const int group = p.num_heads / p.num_kv_heads;
+        split = p.split_heads != 0;
+        first = split && (it.kh & 1) ? group / 2 : 0;
+        last = split && !(it.kh & 1) ? group / 2 : group;
+        if (split) it.kh >>= 1;
     }
 };
 
@@ -862,7 +875,6 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
     constexpr int S_ = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group = p.num_heads / p.num_kv_heads;
     const uint32_t raw = smem_u32(smem);
     if (raw & 1023u) {
         if (threadIdx.x == 0) atomicOr(&s_status_prefill, kStatusSmemAlign);
@@ -870,26 +882,24 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
     }
     const uint32_t bars = smem_u32(smem + C::kBars);
     const uint32_t b_k = bars, b_kfree = b_k + 16, b_full = b_kfree + 16, b_empty = b_full + 8 * S_,
-                   b_s = b_empty + 8 * S_, b_sfree = b_s + 8 * kWBufs, b_part = b_sfree + 8 * kWBufs,
-                   b_pfree = b_part + 8, b_fin = b_pfree + 8;
+                   b_s = b_empty + 8 * S_, b_sfree = b_s + 32, b_fin = b_sfree + 32;
     const ItemBars ib = item_bars(b_fin + 8, smem + C::kItems, kSumWarps + 2);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBars + 8 * C::kNumBars);
     volatile int* dead = reinterpret_cast<volatile int*>(tslot + 1);
+    float* lse = reinterpret_cast<float*>(smem + C::kLse);   // negated, in log2 units
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(b_k + 8 * i, 1);
+            mbar_init(b_k + 8 * i, 2);
             mbar_init(b_kfree + 8 * i, 1);
         }
         for (int i = 0; i < S_; ++i) {
             mbar_init(b_full + 8 * i, 1);
-            mbar_init(b_empty + 8 * i, 1);
+            mbar_init(b_empty + 8 * i, 1 + kSumWarps);   // the product's end, and the readers of lse
         }
-        for (int i = 0; i < kWBufs; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(b_s + 8 * i, 1);
             mbar_init(b_sfree + 8 * i, kSumWarps / 2);
         }
-        mbar_init(b_part, kSumWarps / 2);
-        mbar_init(b_pfree, kSumWarps / 2);
         mbar_init(b_fin, 1);
         *dead = 0;
         fence_barrier_init();
@@ -903,139 +913,121 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
         return __all_sync(0xffffffffu, wait_or_dead(dead, bar, parity));
     };
 
-    if (warp < kSumWarps) {
-        // A thread per key. The two groups of four warps take the steps (head, query tile) in
-        // turn; a key's sum is that of the even steps plus that of the odd ones, whichever
-        // group had them.
-        const int wg = warp >> 2, row = threadIdx.x & 127;
-        float* lq = reinterpret_cast<float*>(smem + C::kLse) + warp * kBlk;  // this warp's own
-        float* part = reinterpret_cast<float*>(smem + C::kPart) + row;
-        const uint32_t ts = tm + ((uint32_t)(32 * (warp & 3)) << 16);
+    if (warp < kSumWarps) {  // two threads per key of key tile w, one per half of the queries' columns
+        const int w = warp >> 3, half = (warp >> 2) & 1, row = threadIdx.x & 127;
+        const int pair_id = 1 + 4 * w + (warp & 3);
+        const uint32_t ts = tm + ((uint32_t)(32 * (warp & 3)) << 16) + 2 * kBlk * w + 64 * half;
+        float* xch = reinterpret_cast<float*>(smem + C::kXch) + kBlk * w + row;
         const float sl = fabsf(p.scale_log2);
         const float2 sl2 = make_float2(sl, sl);
-        uint32_t done = 0;       // steps of the items before
-        uint32_t par_part = 0;
+        Place<S_> at;
+        Place<2> buf;
         bool ok = true;
         for (int n = 0; ok; ++n) {
-            const Item it = take_item(ib, dead, n);
+            Item it = take_item(ib, dead, n);
             if (it.seq == kEnd) break;
             if (it.seq < 0) continue;
             const Queries qs(it, p.last_queries);
-            const int steps = qs.tiles * group;
-            const int key = qs.key0 + row;
-            const int i0 = wg ^ (done & 1);     // this group's first step
+            const Heads hs(it, p);
+            const int key = qs.key0 + w * kBlk + row;
             float sum = 0.f;
-            // the log-sum-exps of a step's queries, four to a lane, negated, in log2 units
-            float mine[4];
-            int h = i0 / qs.tiles, qt = i0 - h * qs.tiles;
-            auto fetch = [&] {
+            for (int h = hs.first; h < hs.last && ok; ++h)
+                for (int qt = 0; qt < qs.tiles; ++qt, at = at.next()) {
+                    if (!(ok = wait(b_full + 8 * at.st, at.par))) break;
+                    if (qs.meets(w, qt)) {
+                        if (!(ok = wait(b_s + 16 * w + 8 * buf.st, buf.par))) break;
+                        tc_fence_after();
+                        const int q0 = qs.q0(qt);
+                        const bool whole = q0 + 1 >= qs.key0 + (w + 1) * kBlk && q0 + kBlk <= qs.len;
+                        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = qs.first + qt * kBlk + 32 * e + lane;
-                    mine[e] = h < group && i < it.len
-                                  ? -kLog2e * __ldg(p.lse + (int64_t)(it.kh * group + h) * p.total_tokens +
-                                                    it.start + i)
-                                  : 0.f;
-                }
-            };
-            fetch();
-            for (int i = i0; i < steps; i += 2) {
-                const int q0 = qs.first + qt * kBlk;
+                        for (int g = 0; g < 2; ++g) {
+                            const int col0 = 64 * half + 32 * g;
+                            const float* lq = lse + at.st * kBlk + col0;
+                            uint32_t s[32];
+                            tmem_ld32(ts + kBlk * buf.st + 32 * g, s);
+                            if (g == 1) {
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(b_sfree + 16 * w + 8 * buf.st);
+                            }
+                            if (whole) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (++qt == qs.tiles) qt = 0, ++h;
-                __syncwarp();  // the previous step's are read
+                                for (int c = 0; c < 32; c += 4) {
+                                    const float4 e = *reinterpret_cast<const float4*>(lq + c);
+                                    const float2 x = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
+                                                          sl2, make_float2(e.x, e.y));
+                                    const float2 y = fma2(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
+                                                          sl2, make_float2(e.z, e.w));
+                                    acc[0] = add2(acc[0], exp2_pair(x, c / 2));
+                                    acc[1] = add2(acc[1], exp2_pair(y, c / 2 + 1));
+                                }
+                            } else {  // the diagonal, or the prompt's end: some columns do not count
+                                const int lo = key - q0 - col0, hi = qs.len - q0 - col0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) lq[32 * e + lane] = mine[e];
-                fetch();
-                __syncwarp();
-                const uint32_t g = done + i, buf = g % kWBufs;
-                if (!(ok = wait(b_s + 8 * buf, (g / kWBufs) & 1))) break;
-                tc_fence_after();
-                const bool whole = q0 >= qs.key0 + kBlk && q0 + kBlk <= it.len;
-                const int lo = key - q0, hi = it.len - q0;   // else: the columns that count
-                float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t s[64];
-                    tmem_ld64_issue(ts + kBlk * buf + 64 * half, s);
-                    tmem_wait_ld(s);
-                    if (half == 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(b_sfree + 8 * buf);
-                    }
-                    if (whole) {
-#pragma unroll
-                        for (int c = 0; c < 64; c += 4) {
-                            const float4 e = *reinterpret_cast<const float4*>(lq + 64 * half + c);
-                            const float2 x = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sl2,
-                                                  make_float2(e.x, e.y));
-                            const float2 y = fma2(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
-                                                  sl2, make_float2(e.z, e.w));
-                            acc[0] = add2(acc[0], exp2_pair<PA_WEIGHTS_POLY>(x, c / 2));
-                            acc[1] = add2(acc[1], exp2_pair<PA_WEIGHTS_POLY>(y, c / 2 + 1));
+                                for (int c = 0; c < 32; ++c) {
+                                    const float x = ex2(fmaf(__uint_as_float(s[c]), sl, lq[c]));
+                                    if (c >= lo && c < hi) acc[c & 1].x += x;
+                                }
+                            }
                         }
-                    } else {  // the diagonal, or the prompt's end
-#pragma unroll
-                        for (int c = 0; c < 64; ++c) {
-                            const int col = 64 * half + c;
-                            const float x = ex2(fmaf(__uint_as_float(s[c]), sl, lq[col]));
-                            if (col >= lo && col < hi) acc[c & 1].x += x;
-                        }
+                        sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+                        buf = buf.next();
                     }
-                }
-                sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-            }
-            if (!ok) break;
-            done += steps;
-            if (steps > 1) {
-                if (i0 == 1) {
-                    if (!(ok = wait(b_pfree, par_part ^ 1))) break;   // (the first wait is for no use yet)
-                    *part = sum;
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(b_part);
-                } else {
-                    if (!(ok = wait(b_part, par_part))) break;
-                    sum += *part;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(b_pfree);
+                    if (lane == 0) mbar_arrive(b_empty + 8 * at.st);
                 }
-                par_part ^= 1;
+            if (half == 1) *xch = sum;
+            if (pair_any(pair_id, !ok)) break;
+            if (half == 0 && key < qs.len) {
+                float* to = p.weights + ((int64_t)it.seq * p.num_kv_heads + it.kh) * p.weights_stride + key;
+                sum += *xch;
+                // two items add to what was zeroed: 0 + a + b is 0 + b + a, bit for bit
+                if (hs.split)
+                    atomicAdd(to, sum);
+                else
+                    *to = sum;
             }
-            if (i0 == 0 && key < it.len)
-                p.weights[((int64_t)it.seq * p.num_kv_heads + it.kh) * p.weights_stride + key] = sum;
+            __syncwarp();
+            named_barrier(pair_id, 64);   // the sums are read before the next ones
         }
     } else if (warp == kSumWarps) {  // products
         const uint32_t idesc = umma_idesc(kBlk, kBlk, false) | (p.scale_log2 < 0.f ? kNegateA : 0u);
         const bool one = elect_one();
-        Place<2> kt;
+        Place<2> kt, buf[2];
         Place<S_> at;
-        Place<kWBufs> buf;
-        int used = 0;
         bool ok = true;
         for (int n = 0; ok; ++n) {
-            const Item it = take_item(ib, dead, n);
+            Item it = take_item(ib, dead, n);
             if (it.seq == kEnd) break;
             if (it.seq < 0) continue;
-            const int steps = Queries(it, p.last_queries).tiles * group;
-            if (!(ok = wait(b_k + 8 * kt.st, kt.par))) break;
-            const uint32_t k_lo = rows_lo(raw + kt.st * C::kTile);
-            for (int i = 0; i < steps; ++i, ++used) {
-                if (used >= kWBufs && !(ok = wait(b_sfree + 8 * buf.st, buf.par ^ 1))) break;
-                if (!(ok = wait(b_full + 8 * at.st, at.par))) break;
-                tc_fence_after();
-                const uint32_t d = tm + kBlk * buf.st, q_lo = rows_lo(raw + C::kRing + at.st * C::kTile);
-                if (one) {
-                    issue_qk<D>(d, k_lo, q_lo, idesc);
-                    umma_commit(b_s + 8 * buf.st);
-                    umma_commit(b_empty + 8 * at.st);
-                    if (i == steps - 1) umma_commit(b_kfree + 8 * kt.st);
+            const Queries qs(it, p.last_queries);
+            const Heads hs(it, p);
+            ok = wait(b_k + 8 * kt.st, kt.par);
+            for (int h = hs.first; h < hs.last && ok; ++h)
+                for (int qt = 0; qt < qs.tiles && ok; ++qt, at = at.next()) {
+                    ok = wait(b_full + 8 * at.st, at.par);
+                    const uint32_t q_lo = rows_lo(raw + C::kRing + at.st * C::kTile);
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        if (!ok || !qs.meets(w, qt)) continue;
+                        // (the first wait of a buffer is for no use yet)
+                        if (!(ok = wait(b_sfree + 16 * w + 8 * buf[w].st, buf[w].par ^ 1))) continue;
+                        tc_fence_after();
+                        const uint32_t d = tm + 2 * kBlk * w + kBlk * buf[w].st;
+                        const uint32_t k_lo = rows_lo(raw + (2 * kt.st + w) * C::kTile);
+                        if (one) {
+                            issue_qk<D>(d, k_lo, q_lo, idesc);
+                            umma_commit(b_s + 16 * w + 8 * buf[w].st);
+                        }
+                        __syncwarp();
+                        buf[w] = buf[w].next();
+                    }
+                    if (ok && one) umma_commit(b_empty + 8 * at.st);
+                    __syncwarp();
                 }
-                __syncwarp();
-                at = at.next();
-                buf = buf.next();
-            }
+            if (ok && one) umma_commit(b_kfree + 8 * kt.st);
+            __syncwarp();
             kt = kt.next();
         }
         if (one) umma_commit(b_fin);
@@ -1051,22 +1043,50 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
         int keys = 0, loaded = 0;
         bool ok = true;
         for (int n = 0; ok; ++n) {
-            const Item it = take_item(ib, dead, n);
+            Item it = take_item(ib, dead, n);
             if (it.seq == kEnd) break;
             if (it.seq < 0) continue;
             const Queries qs(it, p.last_queries);
-            if (keys >= 2 && !(ok = wait(b_kfree + 8 * kt.st, kt.par ^ 1))) break;
-            if (lane == 0)
-                load_tile<D>(raw + kt.st * C::kTile, &kmap, it.kh, it.start + qs.key0, b_k + 8 * kt.st);
+            const Heads hs(it, p);
+            const int head0 = it.kh * (p.num_heads / p.num_kv_heads);
+            float mine[4];
+            auto fetch = [&](int h, int qt) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = qs.q0(qt) + 32 * e + lane;
+                    mine[e] = h < hs.last && i < qs.len
+                                  ? -kLog2e * __ldg(p.lse + (int64_t)(head0 + h) * p.total_tokens + it.start + i)
+                                  : 0.f;
+                }
+            };
+            fetch(hs.first, 0);
+            if (!(ok = wait(b_kfree + 8 * kt.st, kt.par ^ 1))) break;   // (the first two are for no use yet)
+            if (lane == 0) {
+                for (int w = 0; w < 2; ++w) {
+                    if (qs.exists(w))
+                        load_tile<D>(raw + (2 * kt.st + w) * C::kTile, &kmap, it.kh, it.start + qs.key0 + w * kBlk,
+                                     b_k + 8 * kt.st);
+                    else
+                        mbar_arrive(b_k + 8 * kt.st);
+                }
+            }
+            __syncwarp();
             ++keys;
             kt = kt.next();
-            for (int h = 0; h < group && ok; ++h)
+            for (int h = hs.first; h < hs.last && ok; ++h)
                 for (int qt = 0; qt < qs.tiles; ++qt, ++loaded, at = at.next()) {
-                    if (loaded >= S_ && !(ok = wait(b_empty + 8 * at.st, at.par ^ 1))) break;
-                    if (lane == 0)
-                        load_tile<D>(raw + C::kRing + at.st * C::kTile, &qmap, it.kh * group + h,
-                                     it.start + qs.first + qt * kBlk, b_full + 8 * at.st);
+                    if (!(ok = wait(b_empty + 8 * at.st, at.par ^ 1))) break;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) lse[at.st * kBlk + 32 * e + lane] = mine[e];
                     __syncwarp();
+                    if (lane == 0)
+                        load_tile<D>(raw + C::kRing + at.st * C::kTile, &qmap, head0 + h, it.start + qs.q0(qt),
+                                     b_full + 8 * at.st);
+                    __syncwarp();
+                    if (qt + 1 < qs.tiles)
+                        fetch(h, qt + 1);
+                    else
+                        fetch(h + 1, 0);
                 }
         }
         if (lane == 0 && *dead != 0) {  // given up: the loads in flight land before the CTA ends
@@ -1077,8 +1097,8 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
                 landed &= mbar_wait_bounded(b_full + 8 * (i % S_), (i / S_) & 1);
             if (!landed) atomicOr(&s_status_prefill, kStatusTimeout);
         }
-    } else {  // items
-        walk_items(p, ib, dead, false, [](int len) { return (len + kBlk - 1) / kBlk; },
+    } else {  // items: pairs of key tiles
+        walk_items(p, p.split_heads ? 2 * p.num_kv_heads : p.num_kv_heads, ib, dead, false, [](int len) { return (len + 2 * kBlk - 1) / (2 * kBlk); },
                    [](const Item&) { return true; });
     }
     __syncwarp();
@@ -1110,9 +1130,16 @@ cudaError_t launch_weights_t(const PrefillParams& p, const CUtensorMap& qmap, co
     cudaError_t e = cudaFuncSetAttribute(prefill_weights_kernel<D>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (int64_t)(p.total_tokens / kBlk + p.num_seqs) + 1;
-    if (tiles * p.num_kv_heads > INT32_MAX) return cudaErrorInvalidConfiguration;
-    prefill_weights_kernel<D><<<(unsigned)(tiles * p.num_kv_heads), kWThreads, C::kSmem, stream>>>(qmap, kmap, p);
+    PrefillParams q = p;
+    // Half the heads per item where an item is long: with whole groups the longest of 8K under 64/8
+    // heads (512 steps) outlasted the average SM's share (450). Short items (a window)
+    // would only read their keys twice.
+    const int64_t queries = p.last_queries > 0 ? std::min(p.last_queries, p.max_seq_len) : p.max_seq_len;
+    q.split_heads = p.num_heads / p.num_kv_heads >= 2 && queries >= 2048;
+    const int64_t tiles = (int64_t)(p.total_tokens / (2 * kBlk) + p.num_seqs) + 1;   // pairs
+    const int64_t items = tiles * p.num_kv_heads * (q.split_heads ? 2 : 1);
+    if (items > INT32_MAX) return cudaErrorInvalidConfiguration;
+    prefill_weights_kernel<D><<<(unsigned)items, kWThreads, C::kSmem, stream>>>(qmap, kmap, q);
     return cudaGetLastError();
 }
 

@@ -17,8 +17,8 @@
 // bits.
 //
 // Bound by HBM for prompts and by launch latency for a decode step, so: every
-// thread moves units of 16 elements (32 bytes of bf16), the loads of up to
-// kUnroll units are in flight before the table of cosines is needed, and the
+// thread moves units of 16 elements (32 bytes of bf16), kept as loaded until the table of
+// cosines is there; the loads of kUnroll units are in flight at once; and the
 // table (one entry per token and frequency) is computed once per CTA for all
 // heads.
 #include <math.h>
@@ -33,31 +33,35 @@ static __device__ unsigned int s_status_rope;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 3;
+#ifndef PA_ROPE_CTAS
+#define PA_ROPE_CTAS 3
+#endif
+#ifndef PA_ROPE_UNROLL
+#define PA_ROPE_UNROLL 3
+#endif
 constexpr int kMaxTokens = 4;   // tokens per CTA
 constexpr int kMaxHalf = 64;    // frequencies
 
-// 16 elements of a row: two pieces of 8 that lie `second` elements apart.
-struct Unit {
-    int token;      // within the CTA; -1: none
-    int row;        // 0 .. H-1: q, H .. H+Hkv-1: k, then v
-    int at;         // first element
-    int second;     // offset of the other eight
-    int freq;       // first frequency, -1: copied unchanged
-};
-
+// Eight consecutive elements as loaded.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
-    if constexpr (sizeof(T) == 4) {
-        float a[4], b[4];
-        Elem<float>::widen(ld_stream(p), a);
-        Elem<float>::widen(ld_stream(p + 4), b);
+struct Eight {
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = a[i], f[4 + i] = b[i];
-    } else {
-        Elem<__nv_bfloat16>::widen(ld_stream(p), f);
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = ld_stream(p + 16 / sizeof(T) * i);
     }
-}
+    __device__ __forceinline__ void widen(float (&f)[8]) const {
+        if constexpr (sizeof(T) == 4) {
+            float a[4], b[4];
+            Elem<float>::widen(v[0], a);
+            Elem<float>::widen(v[1], b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = a[i], f[4 + i] = b[i];
+        } else {
+            Elem<__nv_bfloat16>::widen(v[0], f);
+        }
+    }
+};
 
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
@@ -95,95 +99,112 @@ __device__ __forceinline__ void store8_codes(uint8_t* p, const float (&f)[8], fl
 }
 
 // grid = (token groups, parts of a token's rows). T: type of q, k, v and q_out;
-// FMT: 0 / 1 = the caches hold T, 2 / 3 = E4M3 / int8 codes.
+// FMT: 0 / 1 = the caches hold T, 2 / 3 = E4M3 / int8 codes. A unit is two pieces of 8
+// elements of a row: both members of eight pairs, or (pairs of neighbours, or no
+// rotation) 16 consecutive elements.
 template <typename T, int FMT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, PA_ROPE_CTAS)
 rope_append_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int kUnroll = sizeof(T) == 4 ? 2 : PA_ROPE_UNROLL;
     __shared__ float2 table[kMaxTokens][kMaxHalf];
     const int token0 = blockIdx.x * p.tokens_per_cta;
     const int ntok = min(p.tokens_per_cta, p.num_tokens - token0);
-    const int upr = p.head_dim / 16;                       // units per row
+    const int lg = p.head_dim == 128 ? 3 : 2;              // units per row: 1 << lg
     const int rows = p.num_heads + 2 * p.num_kv_heads;
     const int rot_units = p.half / 8;
-    const int part = (rows * upr + gridDim.y - 1) / gridDim.y;
-    const int u0 = blockIdx.y * part, per_token = min(part, rows * upr - u0);
-    const int total = per_token > 0 ? per_token * ntok : 0;
+    const int part = ((rows << lg) + gridDim.y - 1) / gridDim.y;
+    const int u0 = blockIdx.y * part, per_token = min(part, (rows << lg) - u0);
 
-    Unit un[kUnroll];
-    float a[kUnroll][8], b[kUnroll][8];
-    auto load = [&](int base) {
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            const int idx = base + k * kThreads + threadIdx.x;
-            un[k].token = -1;
-            if (idx >= total) continue;
-            const int tk = idx / per_token;
-            const int u = u0 + idx - tk * per_token;
-            const int row = u / upr, c = u - row * upr;
-            un[k].token = tk;
-            un[k].row = row;
-            const bool turned = row < p.num_heads + p.num_kv_heads && c < rot_units;
-            un[k].freq = turned ? 8 * c : -1;
-            un[k].at = turned && !p.adjacent ? 8 * c : 16 * c;
-            un[k].second = turned && !p.adjacent ? p.half : 8;
-            const int64_t t = token0 + tk;
-            const T* src;
-            if (row < p.num_heads)
-                src = static_cast<const T*>(p.q) + t * p.q_stride + (int64_t)row * p.head_dim;
-            else if (row < p.num_heads + p.num_kv_heads)
-                src = static_cast<const T*>(p.k) + t * p.k_stride +
-                      (int64_t)(row - p.num_heads) * p.head_dim;
-            else
-                src = static_cast<const T*>(p.v) + t * p.v_stride +
-                      (int64_t)(row - p.num_heads - p.num_kv_heads) * p.head_dim;
-            load8<T>(src + un[k].at, a[k]);
-            load8<T>(src + un[k].at + un[k].second, b[k]);
+    // this thread's next unit: token tk, unit u0 + u
+    int tk = per_token > 0 ? 0 : ntok, u = threadIdx.x;
+    auto settle = [&] {
+        while (tk < ntok && u >= per_token) {
+            u -= per_token;
+            ++tk;
         }
     };
-    load(0);
+    settle();
+    int tks[kUnroll], us[kUnroll];
+    Eight<T> a[kUnroll], b[kUnroll];
+    // the pieces of unit u of a row: first element and the other piece's distance
+    auto pieces = [&](int row, int c, int& at, int& second) {
+        const bool split = row < p.num_heads + p.num_kv_heads && c < rot_units && !p.adjacent;
+        at = split ? 8 * c : 16 * c;
+        second = split ? p.half : 8;
+    };
+    auto load = [&] {
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+            tks[k] = tk;
+            us[k] = u0 + u;
+            if (tk < ntok) {
+                const int row = us[k] >> lg, c = us[k] & ((1 << lg) - 1);
+                int at, second;
+                pieces(row, c, at, second);
+                const int64_t t = token0 + tk;
+                const T* src;
+                if (row < p.num_heads)
+                    src = static_cast<const T*>(p.q) + t * p.q_stride + (int64_t)row * p.head_dim;
+                else if (row < p.num_heads + p.num_kv_heads)
+                    src = static_cast<const T*>(p.k) + t * p.k_stride +
+                          (int64_t)(row - p.num_heads) * p.head_dim;
+                else
+                    src = static_cast<const T*>(p.v) + t * p.v_stride +
+                          (int64_t)(row - p.num_heads - p.num_kv_heads) * p.head_dim;
+                a[k].load(src + at);
+                b[k].load(src + at + second);
+            }
+            u += kThreads;
+            settle();
+        }
+    };
+    load();
     for (int i = threadIdx.x; i < ntok * p.half; i += kThreads) {
-        const int tk = i / p.half, f = i - tk * p.half;
-        const int32_t pos = __ldg(p.positions + (int64_t)p.axis[f] * p.num_tokens + token0 + tk);
+        const int t = i / p.half, f = i - t * p.half;
+        const int32_t pos = __ldg(p.positions + (int64_t)p.axis[f] * p.num_tokens + token0 + t);
         const uint64_t turn = (uint64_t)(int64_t)pos * p.turns[f];
         float s, c;
         sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
-        table[tk][f] = make_float2(c * p.mscale, s * p.mscale);
+        table[t][f] = make_float2(c * p.mscale, s * p.mscale);
     }
     __syncthreads();
-    for (int base = 0; base < total; base += kUnroll * kThreads) {
-        if (base > 0) load(base);
+    while (tks[0] < ntok) {
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k) {
-            if (un[k].token < 0) continue;
-            if (un[k].freq >= 0) {
-                const float2* cs = &table[un[k].token][un[k].freq];
-                if (p.adjacent) {
+            if (tks[k] >= ntok) continue;
+            int row = us[k] >> lg;
+            const int c = us[k] & ((1 << lg) - 1);
+            int at, second;
+            pieces(row, c, at, second);
+            float x[8], y[8];
+            a[k].widen(x);
+            b[k].widen(y);
+            if (row < p.num_heads + p.num_kv_heads && c < rot_units) {
+                const float4* cs = reinterpret_cast<const float4*>(&table[tks[k]][8 * c]);  // two at a time
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 w = cs[j], y = cs[4 + j];
-                        const float x0 = a[k][2 * j], x1 = a[k][2 * j + 1];
-                        const float z0 = b[k][2 * j], z1 = b[k][2 * j + 1];
-                        a[k][2 * j] = x0 * w.x - x1 * w.y;
-                        a[k][2 * j + 1] = x1 * w.x + x0 * w.y;
-                        b[k][2 * j] = z0 * y.x - z1 * y.y;
-                        b[k][2 * j + 1] = z1 * y.x + z0 * y.y;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 w = cs[j];
-                        const float x0 = a[k][j], x1 = b[k][j];
-                        a[k][j] = x0 * w.x - x1 * w.y;
-                        b[k][j] = x1 * w.x + x0 * w.y;
+                for (int j = 0; j < 4; ++j) {
+                    const float4 w = cs[j];
+                    if (p.adjacent) {  // frequencies 2j, 2j + 1: pairs (4j, 4j + 1), (4j + 2, 4j + 3) of x then y
+                        float* z = j < 2 ? x + 4 * j : y + 4 * (j - 2);
+                        const float z0 = z[0], z1 = z[1], z2 = z[2], z3 = z[3];
+                        z[0] = z0 * w.x - z1 * w.y;
+                        z[1] = z1 * w.x + z0 * w.y;
+                        z[2] = z2 * w.z - z3 * w.w;
+                        z[3] = z3 * w.z + z2 * w.w;
+                    } else {
+                        const float x0 = x[2 * j], x1 = x[2 * j + 1], y0 = y[2 * j], y1 = y[2 * j + 1];
+                        x[2 * j] = x0 * w.x - y0 * w.y;
+                        y[2 * j] = y0 * w.x + x0 * w.y;
+                        x[2 * j + 1] = x1 * w.z - y1 * w.w;
+                        y[2 * j + 1] = y1 * w.z + x1 * w.w;
                     }
                 }
             }
-            const int64_t t = token0 + un[k].token;
-            int row = un[k].row;
+            const int64_t t = token0 + tks[k];
             if (row < p.num_heads) {
-                T* dst = static_cast<T*>(p.q_out) + (t * p.num_heads + row) * p.head_dim + un[k].at;
-                store8<T>(dst, a[k]);
-                store8<T>(dst + un[k].second, b[k]);
+                T* dst = static_cast<T*>(p.q_out) + (t * p.num_heads + row) * p.head_dim + at;
+                store8<T>(dst, x);
+                store8<T>(dst + second, y);
                 continue;
             }
             row -= p.num_heads;
@@ -197,18 +218,19 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
             }
             const int64_t blk = slot >> p.log2_block_size;
             const int64_t off = slot & (p.block_size - 1);
-            const int64_t at = ((blk * p.num_kv_heads + row) * p.block_size + off) * p.head_dim + un[k].at;
+            const int64_t to = ((blk * p.num_kv_heads + row) * p.block_size + off) * p.head_dim + at;
             if constexpr (FMT >= 2) {
-                uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + at;
+                uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + to;
                 const float sc = __ldg((is_v ? p.v_scale : p.k_scale) + row);
-                store8_codes<FMT>(dst, a[k], sc);
-                store8_codes<FMT>(dst + un[k].second, b[k], sc);
+                store8_codes<FMT>(dst, x, sc);
+                store8_codes<FMT>(dst + second, y, sc);
             } else {
-                T* dst = static_cast<T*>(is_v ? p.v_cache : p.k_cache) + at;
-                store8<T>(dst, a[k]);
-                store8<T>(dst + un[k].second, b[k]);
+                T* dst = static_cast<T*>(is_v ? p.v_cache : p.k_cache) + to;
+                store8<T>(dst, x);
+                store8<T>(dst + second, y);
             }
         }
+        load();
     }
 }
 

@@ -52,6 +52,7 @@ RAGGED = [
     ([1, 1, 1, 1, 1], 16, 2, 64),
     ([1100], 6, 2, 128),
     ([64] * 40, 2, 2, 128),                       # more prompts than a warp has lanes
+    ([2300, 17], 3, 1, 64),                       # heads of a group in two halves, 1 and 2
 ]
 
 
