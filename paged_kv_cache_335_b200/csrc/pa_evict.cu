@@ -48,15 +48,32 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // ---------------------------------------------------------------------------
 // select
 // ---------------------------------------------------------------------------
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 256;
-constexpr int kListCap = 8192;  // movers listed per round
+// The threshold key is found digit by digit (11, 11 and 10 bits; four of 8 in short contexts,
+// where counting 2048 bins would cost more than a pass over the keys) from histograms in shared
+// memory; the keys lie there too, so that the weights are read once (contexts above what it
+// holds read them again in every pass). A warp owns a run of 32-token words, a lane a
+// token of each, and takes kBatch words at a time: with one load per step a row of 32K
+// took 53 us, each step a memory latency. The first digit is sign, exponent and two
+// bits of a heavy-tailed distribution, a few dozen bins: each bin has kCopies places,
+// so that warps collide less.
+constexpr int kCopies = 4;
+constexpr int kBatch = 8;
+constexpr int kMaxWarps = 32;
+
+template <int kThreads_>
+struct Select {
+    static constexpr int kThreads = kThreads_, kWarps = kThreads / 32;
+    static constexpr int kDigit = kThreads == 256 ? 8 : 11, kBins = 1 << kDigit;
+    static constexpr int kListCap = kThreads == 256 ? 4096 : 8192;  // movers listed per round, where
+                                                                    // the histograms were
+    static_assert(kListCap >= kBins * kCopies && kBins >= kThreads, "histograms");
+};
 
 // Shared memory: [chosen bits: words][holes or movers before a word: words]
-// [mover list: kListCap][histogram: kBins][misc].
+// [histograms, then the mover list: kListCap][scan: kMaxWarps + misc][keys].
+template <int kThreads>
 __device__ __forceinline__ int block_scan_exclusive(int v, int* sm, int& total) {
-    // sm: kSelWarps + 1 ints
+    constexpr int kWarps = kThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = v;
 #pragma unroll
@@ -67,33 +84,192 @@ __device__ __forceinline__ int block_scan_exclusive(int v, int* sm, int& total) 
     if (lane == 31) sm[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        int w = sm[lane];
+        int w = lane < kWarps ? sm[lane] : 0;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, w, off);
             if (lane >= off) w += y;
         }
-        sm[lane] = w;
+        if (lane < kWarps) sm[lane] = w;
     }
     __syncthreads();
-    total = sm[kSelWarps - 1];
+    total = sm[kWarps - 1];
     const int r = x - v + (warp ? sm[warp - 1] : 0);
     __syncthreads();
     return r;
 }
 
-__global__ void __launch_bounds__(kSelThreads, 1)
+// f(word, key, token exists) for each word of the warp's run w0 .. w1, in order; keys of the
+// first `cand` tokens, from shared memory or made of the weights.
+template <bool kShared, typename F>
+__device__ __forceinline__ void each_word(const float* w, const uint32_t* keys, int w0, int w1, int cand, F f) {
+    const int lane = threadIdx.x & 31;
+    for (int i = w0; i < w1; i += kBatch) {
+        uint32_t k[kBatch];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+            const int t = 32 * (i + e) + lane;
+            k[e] = 0u;
+            if (i + e < w1 && t < cand) k[e] = kShared ? keys[t] : weight_key(__ldg(w + t));
+        }
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e)
+            if (i + e < w1) f(i + e, k[e], 32 * (i + e) + lane < cand);
+    }
+}
+
+// Marks the kept candidates of a row in `bits`, with the holes below edge or the movers behind
+// it before each word; returns the number of holes.
+template <int kThreads, bool kShared>
+__device__ __forceinline__ int select_row(const float* w, int cand, int edge, uint32_t* bits, int* before,
+                                          int* hist, int* scan, uint32_t* keys) {
+    using C = Select<kThreads>;
+    constexpr int kWarps = C::kWarps, kBins = C::kBins;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    volatile int* misc = scan + kMaxWarps;  // bin, remaining rank
+    const int words = (cand + 31) / 32;
+    const int wpw = (words + kWarps - 1) / kWarps;
+    const int w0 = min(words, warp * wpw), w1 = min(words, w0 + wpw);
+    if constexpr (kShared) {
+        each_word<false>(w, keys, w0, w1, cand, [&](int i, uint32_t key, bool) { keys[32 * i + lane] = key; });
+        __syncwarp();   // (a warp reads its own words alone)
+    }
+    // The edge-th largest key among the candidates, and how many of the tokens
+    // that hold exactly that key are taken (the lowest indices).
+    uint32_t prefix = 0, known = 0;   // digits found so far and their bits
+    int want = edge;                  // rank of the threshold within the tokens matching `prefix`
+    if (edge > 0) {
+        for (int shift = 32 - C::kDigit; known != 0xffffffffu; shift = max(0, shift - C::kDigit)) {
+            const uint32_t mask = ~known >> shift;   // the digit: the last one may be shorter
+            for (int b = tid; b < kBins; b += kThreads) reinterpret_cast<int4*>(hist)[b] = make_int4(0, 0, 0, 0);
+            __syncthreads();
+            each_word<kShared>(w, keys, w0, w1, cand, [&](int, uint32_t key, bool in) {
+                if (in && (key & known) == prefix)
+                    atomicAdd(&hist[((key >> shift) & mask) * kCopies + (warp & (kCopies - 1))], 1);
+            });
+            __syncthreads();
+            // bins from the top, kBins / kThreads to a thread: the one that holds rank `want`
+            constexpr int kMine = kBins / kThreads;
+            int c[kMine], sum = 0;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const int4 h = reinterpret_cast<const int4*>(hist)[kBins - 1 - (tid * kMine + i)];
+                c[i] = h.x + h.y + h.z + h.w;
+                sum += c[i];
+            }
+            int total;
+            int above = block_scan_exclusive<kThreads>(sum, scan, total);
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                if (above < want && want <= above + c[i]) {
+                    misc[0] = kBins - 1 - (tid * kMine + i);
+                    misc[1] = want - above;
+                }
+                above += c[i];
+            }
+            __syncthreads();
+            prefix |= (uint32_t)misc[0] << shift;
+            want = misc[1];
+            known |= mask << shift;
+            __syncthreads();
+        }
+    }
+    const uint32_t thr = prefix;
+    // Each word's tokens above the threshold and on it, one word per lane in turn (a word costs two
+    // comparisons and two votes; the counting below is a lane's work for a word).
+    int eq_count = 0;
+    for (int i = w0; i < w1; i += 32) {
+        uint32_t mine_gt = 0, mine_eq = 0;
+        each_word<kShared>(w, keys, i, min(i + 32, w1), cand, [&](int j, uint32_t key, bool in) {
+            const uint32_t gt = __ballot_sync(0xffffffffu, in && key > thr);
+            const uint32_t eq = __ballot_sync(0xffffffffu, in && key == thr);
+            if (lane == j - i) {
+                mine_gt = gt;
+                mine_eq = eq;
+            }
+        });
+        if (edge == 0) mine_gt = mine_eq = 0;
+        if (i + lane < w1) {
+            bits[i + lane] = mine_gt;
+            before[i + lane] = (int)mine_eq;
+        }
+        eq_count += __popc(mine_eq);
+    }
+    int total;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) eq_count += __shfl_xor_sync(0xffffffffu, eq_count, off);
+    // lane 0 carries the warp's count: exclusive prefix over the warps
+    int eq_before = block_scan_exclusive<kThreads>(lane == 0 ? eq_count : 0, scan, total);
+    eq_before = __shfl_sync(0xffffffffu, eq_before, 0);
+    // inclusive sum over the lanes
+    auto lanes_sum = [&](int x) {
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+        }
+        return x;
+    };
+    auto below_mask = [&](int i) {  // tokens of word i below edge: holes count there, movers above it
+        const int below = max(0, min(32, edge - 32 * i));
+        return below == 32 ? 0xffffffffu : (1u << below) - 1u;
+    };
+    int holes = 0, movers = 0;
+    for (int i = w0; i < w1; i += 32) {
+        const bool have = i + lane < w1;
+        uint32_t eq = have ? (uint32_t)before[i + lane] : 0u;
+        const int sum = lanes_sum(__popc(eq));
+        // of the equal ones the lowest `want` are taken; one word at most is cut
+        int take = want - (eq_before + sum - __popc(eq));
+        if (take <= 0) eq = 0;
+        for (; __popc(eq) > take && eq != 0; eq &= ~(0x80000000u >> __clz(eq))) {
+        }
+        eq_before += __shfl_sync(0xffffffffu, sum, 31);
+        if (have) {
+            const uint32_t cm = bits[i + lane] | eq, bm = below_mask(i + lane);
+            bits[i + lane] = cm;
+            holes += __popc(~cm & bm);
+            movers += __popc(cm & ~bm);
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        holes += __shfl_xor_sync(0xffffffffu, holes, off);
+        movers += __shfl_xor_sync(0xffffffffu, movers, off);
+    }
+    // holes before each word below edge, movers before each word above it (the
+    // word that holds edge itself counts movers; its holes come last)
+    int hb = block_scan_exclusive<kThreads>(lane == 0 ? holes : 0, scan, total);
+    const int num_holes = total;
+    int mb = block_scan_exclusive<kThreads>(lane == 0 ? movers : 0, scan, total);
+    hb = __shfl_sync(0xffffffffu, hb, 0);
+    mb = __shfl_sync(0xffffffffu, mb, 0);
+    for (int i = w0; i < w1; i += 32) {
+        const bool have = i + lane < w1;
+        const uint32_t bm = below_mask(i + lane), cm = have ? bits[i + lane] : bm;
+        const int h = __popc(~cm & bm), m = have ? __popc(cm & ~bm) : 0;
+        const int hs = lanes_sum(h), ms = lanes_sum(m);
+        if (have) before[i + lane] = bm == 0xffffffffu ? hb + hs - h : mb + ms - m;
+        hb += __shfl_sync(0xffffffffu, hs, 31);
+        mb += __shfl_sync(0xffffffffu, ms, 31);
+    }
+    __syncthreads();
+    return num_holes;
+}
+
+template <int kThreads, bool kShared>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 5 : 1)
 evict_select_kernel(const EvictParams p) {
+    constexpr int kWarps = kThreads / 32, kListCap = Select<kThreads>::kListCap;
     extern __shared__ __align__(16) uint32_t sm_u[];
     const int kh = blockIdx.x, s = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int words_cap = (p.max_context_len + 31) / 32;
+    const int words_cap = (p.max_context_len + 127) / 128 * 4;   // (the list stays 16-byte aligned)
     uint32_t* bits = sm_u;                                    // chosen tokens
-    int* before = reinterpret_cast<int*>(bits + words_cap);   // per word: see below
+    int* before = reinterpret_cast<int*>(bits + words_cap);
     int* list = before + words_cap;
-    int* hist = list + kListCap;
-    int* scan = hist + kBins;                                 // kSelWarps
-    volatile int* misc = scan + kSelWarps;                    // bin, remaining
+    int* scan = list + kListCap;
+    asm volatile("griddepcontrol.launch_dependents;");
     const int n = clamp_len(__ldg(p.context_lens + s), p.max_context_len, tid == 0 && kh == 0);
     const int64_t row = (int64_t)s * p.num_kv_heads + kh;
     const float* w = p.weights + row * p.weights_stride;
@@ -102,114 +278,20 @@ evict_select_kernel(const EvictParams p) {
     const int new_n = min(n, p.budget);
     if (kh == 0 && tid == 0) p.new_context_lens[s] = new_n;
     if (n <= p.budget) {  // nothing to evict
-        for (int j = tid; j < p.budget; j += kSelThreads) kept[j] = j < n ? j : -1;
+        for (int j = tid; j < p.budget; j += kThreads) kept[j] = j < n ? j : -1;
         if (wo != w)
-            for (int j = tid; j < n; j += kSelThreads) wo[j] = w[j];
-        for (int j = n + tid; j < p.weights_stride; j += kSelThreads) wo[j] = 0.f;
+            for (int j = tid; j < n; j += kThreads) wo[j] = w[j];
+        for (int64_t j = n + tid; j < p.weights_stride; j += kThreads) wo[j] = 0.f;
         return;
     }
     const int edge = p.budget - p.recent, cand = n - p.recent;  // cand > edge
     const int words = (cand + 31) / 32;
-
-    // The edge-th largest key among the candidates, and how many of the tokens
-    // that hold exactly that key are taken (the lowest indices).
-    uint32_t prefix = 0;
-    int want = edge;  // rank of the threshold within the tokens matching `prefix`
-    if (edge > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int b = tid; b < kBins; b += kSelThreads) hist[b] = 0;
-            __syncthreads();
-            const uint32_t high = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-            for (int t = tid; t < cand; t += kSelThreads) {
-                const uint32_t key = weight_key(w[t]);
-                if ((key & high) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1);
-            }
-            __syncthreads();
-            if (warp == 0) {  // bins from the top: the one that holds rank `want`
-                int c[8], sum = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    c[i] = hist[255 - (lane * 8 + i)];
-                    sum += c[i];
-                }
-                int x = sum;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, x, off);
-                    if (lane >= off) x += y;
-                }
-                int above = x - sum;
-                if (above < want && want <= x) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (above < want && want <= above + c[i]) {
-                            misc[0] = 255 - (lane * 8 + i);
-                            misc[1] = want - above;
-                        }
-                        above += c[i];
-                    }
-                }
-            }
-            __syncthreads();
-            prefix |= (uint32_t)misc[0] << shift;
-            want = misc[1];
-            __syncthreads();
-        }
-    }
-    const uint32_t thr = prefix;
-    // Equal keys before each word (a warp owns a run of words; lane = token).
-    const int wpw = (words + kSelWarps - 1) / kSelWarps;
-    const int w0 = min(words, warp * wpw), w1 = min(words, w0 + wpw);
-    int eq_count = 0;
-    for (int i = w0; i < w1; ++i) {
-        const int t = 32 * i + lane;
-        const bool eq = edge > 0 && t < cand && weight_key(w[t]) == thr;
-        eq_count += __popc(__ballot_sync(0xffffffffu, eq));
-    }
-    int total;
-    // lane 0 carries the warp's count: exclusive prefix over the warps
-    int eq_before = block_scan_exclusive(lane == 0 ? eq_count : 0, scan, total);
-    eq_before = __shfl_sync(0xffffffffu, eq_before, 0);
-    int holes = 0, movers = 0;
-    for (int i = w0; i < w1; ++i) {
-        const int t = 32 * i + lane;
-        const uint32_t key = t < cand ? weight_key(w[t]) : 0u;
-        const bool eq = edge > 0 && t < cand && key == thr;
-        const uint32_t em = __ballot_sync(0xffffffffu, eq);
-        const int rank = eq_before + __popc(em & ((1u << lane) - 1u));
-        const bool take = edge > 0 && t < cand && (key > thr || (eq && rank < want));
-        const uint32_t cm = __ballot_sync(0xffffffffu, take);
-        eq_before += __popc(em);
-        // tokens of this word below edge: holes count there, movers above it
-        const int below = max(0, min(32, edge - 32 * i));
-        const uint32_t bm = below == 32 ? 0xffffffffu : (1u << below) - 1u;
-        if (lane == 0) {
-            bits[i] = cm;
-            before[i] = 0;
-        }
-        holes += __popc(~cm & bm);
-        movers += __popc(cm & ~bm);
-    }
-    // holes before each word below edge, movers before each word above it (the
-    // word that holds edge itself counts movers; its holes come last)
-    int hb = block_scan_exclusive(lane == 0 ? holes : 0, scan, total);
-    const int num_holes = total;
-    int mb = block_scan_exclusive(lane == 0 ? movers : 0, scan, total);
-    hb = __shfl_sync(0xffffffffu, hb, 0);
-    mb = __shfl_sync(0xffffffffu, mb, 0);
-    for (int i = w0; i < w1; ++i) {
-        const uint32_t cm = bits[i];
-        const int below = max(0, min(32, edge - 32 * i));
-        const uint32_t bm = below == 32 ? 0xffffffffu : (1u << below) - 1u;
-        if (lane == 0) before[i] = below == 32 ? hb : mb;
-        hb += __popc(~cm & bm);
-        mb += __popc(cm & ~bm);
-    }
-    __syncthreads();
+    const int num_holes = select_row<kThreads, kShared>(
+        w, cand, edge, bits, before, list, scan, reinterpret_cast<uint32_t*>(scan + kMaxWarps + 4));
     const int edge_word = edge / 32;
     // The i-th mover goes to the i-th hole, kListCap of them per round.
     for (int r0 = 0; r0 < num_holes; r0 += kListCap) {
-        for (int i = edge_word + warp; i < words; i += kSelWarps) {
+        for (int i = edge_word + warp; i < words; i += kWarps) {
             const int below = max(0, min(32, edge - 32 * i));
             const uint32_t bm = below == 32 ? 0xffffffffu : (1u << below) - 1u;
             const uint32_t m = bits[i] & ~bm;
@@ -217,35 +299,48 @@ evict_select_kernel(const EvictParams p) {
             if ((m >> lane & 1u) && rank >= 0 && rank < kListCap) list[rank] = 32 * i + lane;
         }
         __syncthreads();
-        for (int i = warp; 32 * i < edge; i += kSelWarps) {
-            const int below = min(32, edge - 32 * i);
-            const uint32_t bm = below == 32 ? 0xffffffffu : (1u << below) - 1u;
-            const uint32_t h = ~bits[i] & bm;
-            // the word that holds edge: its holes are the last ones
-            const int base = below == 32 ? before[i] : num_holes - __popc(h);
-            const int rank = base + __popc(h & ((1u << lane) - 1u)) - r0;
-            const int j = 32 * i + lane;
-            if (h >> lane & 1u) {
-                if (rank >= 0 && rank < kListCap) {
-                    const int src = list[rank];
-                    kept[j] = src;
-                    wo[j] = w[src];  // src >= edge > j: not yet overwritten
+        // (kPlaced words at a time, their weights in flight together)
+        constexpr int kPlaced = 4;
+        for (int i0 = warp; 32 * i0 < edge; i0 += kPlaced * kWarps) {
+            int src[kPlaced];
+            float v[kPlaced];
+#pragma unroll
+            for (int e = 0; e < kPlaced; ++e) {
+                const int i = i0 + e * kWarps, j = 32 * i + lane;
+                src[e] = -1;
+                if (32 * i >= edge) continue;
+                const int below = min(32, edge - 32 * i);
+                const uint32_t bm = below == 32 ? 0xffffffffu : (1u << below) - 1u;
+                const uint32_t h = ~bits[i] & bm;
+                // the word that holds edge: its holes are the last ones
+                const int base = below == 32 ? before[i] : num_holes - __popc(h);
+                const int rank = base + __popc(h & ((1u << lane) - 1u)) - r0;
+                if (h >> lane & 1u) {
+                    if (rank >= 0 && rank < kListCap) src[e] = list[rank];
+                } else if (r0 == 0 && j < edge) {
+                    src[e] = j;
                 }
-            } else if (r0 == 0 && j < edge) {
-                kept[j] = j;
-                if (wo != w) wo[j] = w[j];
+                // (a mover's place is >= edge: not yet overwritten when the weights are in place)
+                if (src[e] >= 0) v[e] = w[src[e]];
+            }
+#pragma unroll
+            for (int e = 0; e < kPlaced; ++e) {
+                const int j = 32 * (i0 + e * kWarps) + lane;
+                if (src[e] < 0) continue;
+                kept[j] = src[e];
+                wo[j] = v[e];
             }
         }
         __syncthreads();
     }
     if (num_holes == 0)
-        for (int j = tid; j < edge; j += kSelThreads) {
+        for (int j = tid; j < edge; j += kThreads) {
             kept[j] = j;
             if (wo != w) wo[j] = w[j];
         }
     __syncthreads();
     // recent tokens, ascending (in place, a chunk is read before it is written)
-    for (int j0 = 0; j0 < p.recent; j0 += kSelThreads) {
+    for (int j0 = 0; j0 < p.recent; j0 += kThreads) {
         const int j = j0 + tid;
         float v = 0.f;
         if (j < p.recent) {
@@ -256,7 +351,7 @@ evict_select_kernel(const EvictParams p) {
         if (j < p.recent) wo[edge + j] = v;
         __syncthreads();
     }
-    for (int j = p.budget + tid; j < p.weights_stride; j += kSelThreads) wo[j] = 0.f;
+    for (int64_t j = p.budget + tid; j < p.weights_stride; j += kThreads) wo[j] = 0.f;
 }
 
 // ---------------------------------------------------------------------------
@@ -278,6 +373,8 @@ __device__ __forceinline__ int64_t row_of(const EvictParams& p, int s, int kh, i
 constexpr int kFillWarps = 8;
 __global__ void __launch_bounds__(kFillWarps * 32)
 evict_fill_kernel(const EvictParams p) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int kh = blockIdx.y, s = blockIdx.z;
     const int lane = threadIdx.x & 31;
     const int edge = p.budget - p.recent;
@@ -332,6 +429,7 @@ constexpr int kShiftThreads = 512;
 constexpr int kShiftU = 8;
 __global__ void __launch_bounds__(kShiftThreads)
 evict_shift_kernel(const EvictParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int kh = blockIdx.y, s = blockIdx.z;
     const int n = clamp_len(__ldg(p.context_lens + s), p.max_context_len, false);
     if (n <= p.budget) return;
@@ -368,7 +466,7 @@ evict_shift_kernel(const EvictParams p) {
 // lse the log-sum-exp (log2 units) of the head's partitions: the decode kernel left
 // every score (log2 units) and each partition's running max and sum.
 constexpr int kAddThreads = 256;
-constexpr int kAddTokens = 4;  // per thread
+constexpr int kAddTokens = 4;  // per thread, consecutive: one 16-byte load per head
 constexpr int kMaxHeads = 32;  // of a group, per round
 
 __global__ void __launch_bounds__(kAddThreads)
@@ -378,14 +476,11 @@ add_weights_kernel(const AddWeightsParams p) {
     const int kh = blockIdx.y, s = blockIdx.z;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n = clamp_len(__ldg(p.context_lens + s), p.max_context_len, false);
-    const int t0 = blockIdx.x * kAddThreads * kAddTokens;
-    if (t0 >= n) return;
+    if ((int)(blockIdx.x * kAddThreads * kAddTokens) >= n) return;
+    const int t = (blockIdx.x * kAddThreads + threadIdx.x) * kAddTokens;
     const int group = p.num_heads / p.num_kv_heads;
     const int parts = (n + p.partition_size - 1) / p.partition_size;
-    float* w = p.weights + ((int64_t)s * p.num_kv_heads + kh) * p.weights_stride;
-    float acc[kAddTokens];
-#pragma unroll
-    for (int u = 0; u < kAddTokens; ++u) acc[u] = 0.f;
+    float acc[kAddTokens] = {0.f, 0.f, 0.f, 0.f};
     for (int h0 = 0; h0 < group; h0 += kMaxHeads) {
         const int heads = min(kMaxHeads, group - h0);
         for (int h = warp; h < heads; h += kAddThreads / 32) {
@@ -403,52 +498,90 @@ add_weights_kernel(const AddWeightsParams p) {
             if (lane == 0) lse[h] = L == 0.f ? INFINITY : M + log2f(L);
         }
         __syncthreads();
-        const float* sc = p.scores + ((int64_t)s * p.num_heads + kh * group + h0) * p.score_stride;
-        for (int h = 0; h < heads; ++h) {
-            const float e = lse[h];
-#pragma unroll
-            for (int u = 0; u < kAddTokens; ++u) {
-                const int t = t0 + u * kAddThreads + threadIdx.x;
-                if (t < n) acc[u] += exp2f(__ldg(sc + (int64_t)h * p.score_stride + t) - e);
+        if (t < n) {
+            const float* sc = p.scores + ((int64_t)s * p.num_heads + kh * group + h0) * p.score_stride + t;
+#pragma unroll 8
+            for (int h = 0; h < heads; ++h) {
+                const float4 x = __ldcs(reinterpret_cast<const float4*>(sc + (int64_t)h * p.score_stride));
+                const float e = lse[h];
+                acc[0] += exp2f(x.x - e);
+                acc[1] += exp2f(x.y - e);
+                acc[2] += exp2f(x.z - e);
+                acc[3] += exp2f(x.w - e);
             }
         }
         __syncthreads();
     }
+    float* w = p.weights + ((int64_t)s * p.num_kv_heads + kh) * p.weights_stride + t;
+    if (t + kAddTokens <= n && (reinterpret_cast<uintptr_t>(w) & 15u) == 0) {
+        float4 x = *reinterpret_cast<float4*>(w);
+        x.x += acc[0];
+        x.y += acc[1];
+        x.z += acc[2];
+        x.w += acc[3];
+        *reinterpret_cast<float4*>(w) = x;
+    } else {
 #pragma unroll
-    for (int u = 0; u < kAddTokens; ++u) {
-        const int t = t0 + u * kAddThreads + threadIdx.x;
-        if (t < n) w[t] += acc[u];
+        for (int u = 0; u < kAddTokens; ++u)
+            if (t + u < n) w[u] += acc[u];
     }
 }
 
 }  // namespace
 
-static size_t evict_smem_bytes(int max_context_len) {
-    const size_t words = ((size_t)max_context_len + 31) / 32;
-    return 4 * (2 * words + kListCap + kBins + kSelWarps + 4);
+template <int kThreads>
+static size_t evict_smem_bytes(int max_context_len, bool keys) {
+    const size_t words = ((size_t)max_context_len + 127) / 128 * 4;
+    return 4 * (2 * words + Select<kThreads>::kListCap + kMaxWarps + 4 + (keys ? 32 * words : 0));
 }
 
-int evict_max_context() { return (int)((227 * 1024 - evict_smem_bytes(0)) / 8 * 32); }
+int evict_max_context() { return (int)((227 * 1024 - evict_smem_bytes<1024>(0, false)) / 32 * 128); }
 
-cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
-    const size_t smem = evict_smem_bytes(p.max_context_len);
-    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel,
+// A kernel that starts while the one before it ends (it waits for it itself).
+template <typename K>
+static cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                                    const EvictParams& p) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int kThreads, bool kShared>
+static cudaError_t launch_select(const EvictParams& p, cudaStream_t stream) {
+    const size_t smem = evict_smem_bytes<kThreads>(p.max_context_len, kShared);
+    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<kThreads, kShared>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
+    evict_select_kernel<kThreads, kShared>
+        <<<dim3((unsigned)p.num_kv_heads, (unsigned)p.num_seqs), kThreads, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
     const dim3 rows((unsigned)p.num_kv_heads, (unsigned)p.num_seqs);
-    evict_select_kernel<<<rows, kSelThreads, smem, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    // a row of a short context is bound by its barriers: fewer threads, more rows per SM
+    cudaError_t e = p.max_context_len <= 4096 ? launch_select<256, true>(p, stream)
+                    : evict_smem_bytes<1024>(p.max_context_len, true) <= 227 * 1024
+                        ? launch_select<1024, true>(p, stream)
+                        : launch_select<1024, false>(p, stream);
+    if (e != cudaSuccess) return e;
     if (p.max_context_len <= p.budget) return cudaSuccess;  // no sequence is over its budget
     const int edge = p.budget - p.recent;
     if (edge > 0) {
         const unsigned chunks = (unsigned)((edge + kFillWarps * 32 - 1) / (kFillWarps * 32));
-        evict_fill_kernel<<<dim3(chunks, rows.x, rows.y), kFillWarps * 32, 0, stream>>>(p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = launch_dependent(evict_fill_kernel, dim3(chunks, rows.x, rows.y), kFillWarps * 32, 0, stream, p);
+        if (e != cudaSuccess) return e;
     }
-    if (p.recent > 0) {
-        evict_shift_kernel<<<dim3(2, rows.x, rows.y), kShiftThreads, 0, stream>>>(p);
-        e = cudaGetLastError();
-    }
+    if (p.recent > 0)
+        e = launch_dependent(evict_shift_kernel, dim3(2, rows.x, rows.y), kShiftThreads, 0, stream, p);
     return e;
 }
 

@@ -18,9 +18,8 @@
 //
 // Bound by HBM for prompts and by launch latency for a decode step, so: every
 // thread moves units of 16 elements (32 bytes of bf16), kept as loaded until the table of
-// cosines is there; the loads of kUnroll units are in flight at once; and the
-// table (one entry per token and frequency) is computed once per CTA for all
-// heads.
+// cosines is there, and the table (one entry per token and frequency) is computed once per
+// CTA for all heads.
 #include <math.h>
 
 #include "pa_device.cuh"
@@ -33,12 +32,10 @@ static __device__ unsigned int s_status_rope;
 namespace {
 
 constexpr int kThreads = 256;
-#ifndef PA_ROPE_CTAS
-#define PA_ROPE_CTAS 3
-#endif
-#ifndef PA_ROPE_UNROLL
-#define PA_ROPE_UNROLL 3
-#endif
+// CTAs per SM. Loads in flight come from many threads with one unit each: 16K tokens of
+// 64/8 heads (671 MB) take 129 us = 5.2 TB/s at 5 CTAs, 134 at 4, 185 at 6 (spilled); two
+// units per thread at 4 CTAs 136, three at 3 CTAs 152 us.
+constexpr int kCtas = 5;
 constexpr int kMaxTokens = 4;   // tokens per CTA
 constexpr int kMaxHalf = 64;    // frequencies
 
@@ -103,9 +100,8 @@ __device__ __forceinline__ void store8_codes(uint8_t* p, const float (&f)[8], fl
 // elements of a row: both members of eight pairs, or (pairs of neighbours, or no
 // rotation) 16 consecutive elements.
 template <typename T, int FMT>
-__global__ void __launch_bounds__(kThreads, PA_ROPE_CTAS)
+__global__ void __launch_bounds__(kThreads, kCtas)
 rope_append_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int kUnroll = sizeof(T) == 4 ? 2 : PA_ROPE_UNROLL;
     __shared__ float2 table[kMaxTokens][kMaxHalf];
     const int token0 = blockIdx.x * p.tokens_per_cta;
     const int ntok = min(p.tokens_per_cta, p.num_tokens - token0);
@@ -115,48 +111,41 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
     const int part = ((rows << lg) + gridDim.y - 1) / gridDim.y;
     const int u0 = blockIdx.y * part, per_token = min(part, (rows << lg) - u0);
 
-    // this thread's next unit: token tk, unit u0 + u
+    // this thread's unit: token tk, unit u0 + u
     int tk = per_token > 0 ? 0 : ntok, u = threadIdx.x;
-    auto settle = [&] {
+    Eight<T> a, b;
+    // a unit's row and piece of it, its first element and the other piece's distance
+    struct Place {
+        int row, c, at, second;
+    };
+    auto place = [&] {
+        Place r;
+        r.row = (u0 + u) >> lg;
+        r.c = (u0 + u) & ((1 << lg) - 1);
+        const bool split = r.row < p.num_heads + p.num_kv_heads && r.c < rot_units && !p.adjacent;
+        r.at = split ? 8 * r.c : 16 * r.c;
+        r.second = split ? p.half : 8;
+        return r;
+    };
+    auto load = [&] {  // the first unit at or behind (tk, u)
         while (tk < ntok && u >= per_token) {
             u -= per_token;
             ++tk;
         }
-    };
-    settle();
-    int tks[kUnroll], us[kUnroll];
-    Eight<T> a[kUnroll], b[kUnroll];
-    // the pieces of unit u of a row: first element and the other piece's distance
-    auto pieces = [&](int row, int c, int& at, int& second) {
-        const bool split = row < p.num_heads + p.num_kv_heads && c < rot_units && !p.adjacent;
-        at = split ? 8 * c : 16 * c;
-        second = split ? p.half : 8;
-    };
-    auto load = [&] {
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            tks[k] = tk;
-            us[k] = u0 + u;
-            if (tk < ntok) {
-                const int row = us[k] >> lg, c = us[k] & ((1 << lg) - 1);
-                int at, second;
-                pieces(row, c, at, second);
-                const int64_t t = token0 + tk;
-                const T* src;
-                if (row < p.num_heads)
-                    src = static_cast<const T*>(p.q) + t * p.q_stride + (int64_t)row * p.head_dim;
-                else if (row < p.num_heads + p.num_kv_heads)
-                    src = static_cast<const T*>(p.k) + t * p.k_stride +
-                          (int64_t)(row - p.num_heads) * p.head_dim;
-                else
-                    src = static_cast<const T*>(p.v) + t * p.v_stride +
-                          (int64_t)(row - p.num_heads - p.num_kv_heads) * p.head_dim;
-                a[k].load(src + at);
-                b[k].load(src + at + second);
-            }
-            u += kThreads;
-            settle();
-        }
+        if (tk >= ntok) return;
+        const Place r = place();
+        const int64_t t = token0 + tk;
+        const T* src;
+        if (r.row < p.num_heads)
+            src = static_cast<const T*>(p.q) + t * p.q_stride + (int64_t)r.row * p.head_dim;
+        else if (r.row < p.num_heads + p.num_kv_heads)
+            src = static_cast<const T*>(p.k) + t * p.k_stride +
+                  (int64_t)(r.row - p.num_heads) * p.head_dim;
+        else
+            src = static_cast<const T*>(p.v) + t * p.v_stride +
+                  (int64_t)(r.row - p.num_heads - p.num_kv_heads) * p.head_dim;
+        a.load(src + r.at);
+        b.load(src + r.at + r.second);
     };
     load();
     for (int i = threadIdx.x; i < ntok * p.half; i += kThreads) {
@@ -168,69 +157,63 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
         table[t][f] = make_float2(c * p.mscale, s * p.mscale);
     }
     __syncthreads();
-    while (tks[0] < ntok) {
+    for (; tk < ntok; u += kThreads, load()) {
+        const Place r = place();
+        int row = r.row;
+        const int c = r.c, at = r.at, second = r.second;
+        float x[8], y[8];
+        a.widen(x);
+        b.widen(y);
+        if (row < p.num_heads + p.num_kv_heads && c < rot_units) {
+            const float4* cs = reinterpret_cast<const float4*>(&table[tk][8 * c]);  // two at a time
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            if (tks[k] >= ntok) continue;
-            int row = us[k] >> lg;
-            const int c = us[k] & ((1 << lg) - 1);
-            int at, second;
-            pieces(row, c, at, second);
-            float x[8], y[8];
-            a[k].widen(x);
-            b[k].widen(y);
-            if (row < p.num_heads + p.num_kv_heads && c < rot_units) {
-                const float4* cs = reinterpret_cast<const float4*>(&table[tks[k]][8 * c]);  // two at a time
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 w = cs[j];
-                    if (p.adjacent) {  // frequencies 2j, 2j + 1: pairs (4j, 4j + 1), (4j + 2, 4j + 3) of x then y
-                        float* z = j < 2 ? x + 4 * j : y + 4 * (j - 2);
-                        const float z0 = z[0], z1 = z[1], z2 = z[2], z3 = z[3];
-                        z[0] = z0 * w.x - z1 * w.y;
-                        z[1] = z1 * w.x + z0 * w.y;
-                        z[2] = z2 * w.z - z3 * w.w;
-                        z[3] = z3 * w.z + z2 * w.w;
-                    } else {
-                        const float x0 = x[2 * j], x1 = x[2 * j + 1], y0 = y[2 * j], y1 = y[2 * j + 1];
-                        x[2 * j] = x0 * w.x - y0 * w.y;
-                        y[2 * j] = y0 * w.x + x0 * w.y;
-                        x[2 * j + 1] = x1 * w.z - y1 * w.w;
-                        y[2 * j + 1] = y1 * w.z + x1 * w.w;
-                    }
+            for (int j = 0; j < 4; ++j) {
+                const float4 w = cs[j];
+                if (p.adjacent) {  // frequencies 2j, 2j + 1: pairs (4j, 4j + 1), (4j + 2, 4j + 3) of x then y
+                    float* z = j < 2 ? x + 4 * j : y + 4 * (j - 2);
+                    const float z0 = z[0], z1 = z[1], z2 = z[2], z3 = z[3];
+                    z[0] = z0 * w.x - z1 * w.y;
+                    z[1] = z1 * w.x + z0 * w.y;
+                    z[2] = z2 * w.z - z3 * w.w;
+                    z[3] = z3 * w.z + z2 * w.w;
+                } else {
+                    const float x0 = x[2 * j], x1 = x[2 * j + 1], y0 = y[2 * j], y1 = y[2 * j + 1];
+                    x[2 * j] = x0 * w.x - y0 * w.y;
+                    y[2 * j] = y0 * w.x + x0 * w.y;
+                    x[2 * j + 1] = x1 * w.z - y1 * w.w;
+                    y[2 * j + 1] = y1 * w.z + x1 * w.w;
                 }
             }
-            const int64_t t = token0 + tks[k];
-            if (row < p.num_heads) {
-                T* dst = static_cast<T*>(p.q_out) + (t * p.num_heads + row) * p.head_dim + at;
-                store8<T>(dst, x);
-                store8<T>(dst + second, y);
-                continue;
-            }
-            row -= p.num_heads;
-            const bool is_v = row >= p.num_kv_heads;
-            if (is_v) row -= p.num_kv_heads;
-            const int64_t slot = __ldg(p.slot_mapping + t);
-            if (slot < 0) continue;  // padding token
-            if (slot >= p.num_slots) {
-                atomicOr(&s_status_rope, kStatusBadIndex);
-                continue;
-            }
-            const int64_t blk = slot >> p.log2_block_size;
-            const int64_t off = slot & (p.block_size - 1);
-            const int64_t to = ((blk * p.num_kv_heads + row) * p.block_size + off) * p.head_dim + at;
-            if constexpr (FMT >= 2) {
-                uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + to;
-                const float sc = __ldg((is_v ? p.v_scale : p.k_scale) + row);
-                store8_codes<FMT>(dst, x, sc);
-                store8_codes<FMT>(dst + second, y, sc);
-            } else {
-                T* dst = static_cast<T*>(is_v ? p.v_cache : p.k_cache) + to;
-                store8<T>(dst, x);
-                store8<T>(dst + second, y);
-            }
         }
-        load();
+        const int64_t t = token0 + tk;
+        if (row < p.num_heads) {
+            T* dst = static_cast<T*>(p.q_out) + (t * p.num_heads + row) * p.head_dim + at;
+            store8<T>(dst, x);
+            store8<T>(dst + second, y);
+            continue;
+        }
+        row -= p.num_heads;
+        const bool is_v = row >= p.num_kv_heads;
+        if (is_v) row -= p.num_kv_heads;
+        const int64_t slot = __ldg(p.slot_mapping + t);
+        if (slot < 0) continue;  // padding token
+        if (slot >= p.num_slots) {
+            atomicOr(&s_status_rope, kStatusBadIndex);
+            continue;
+        }
+        const int64_t blk = slot >> p.log2_block_size;
+        const int64_t off = slot & (p.block_size - 1);
+        const int64_t to = ((blk * p.num_kv_heads + row) * p.block_size + off) * p.head_dim + at;
+        if constexpr (FMT >= 2) {
+            uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + to;
+            const float sc = __ldg((is_v ? p.v_scale : p.k_scale) + row);
+            store8_codes<FMT>(dst, x, sc);
+            store8_codes<FMT>(dst + second, y, sc);
+        } else {
+            T* dst = static_cast<T*>(is_v ? p.v_cache : p.k_cache) + to;
+            store8<T>(dst, x);
+            store8<T>(dst + second, y);
+        }
     }
 }
 
