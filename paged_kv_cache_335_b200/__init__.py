@@ -205,8 +205,8 @@ def _dtype_code(t) -> int:
 def _on_current_device(t, name: str):
     """The library launches on the current device and stream: a tensor of another
     GPU would hand its kernels a pointer they cannot use."""
-    cur = _torch().cuda.current_device()
-    if t.device.index != cur:
+    cur = _torch()._C._cuda_getDevice()
+    if t.get_device() != cur:
         raise ValueError(f"{name} is on {t.device}, but the current CUDA device is cuda:{cur}; "
                          "call under torch.cuda.device(...) of the tensors' device")
 
@@ -219,7 +219,7 @@ def _dev(t, name: str, dtype=None):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _addressable(t, name: str):
@@ -234,18 +234,17 @@ def _addressable(t, name: str):
 
 
 def _stream(stream):
-    torch = _torch()
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    if stream is None:  # the current stream's handle, without building a stream object
+        c = _torch()._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def cache_desc(k_cache) -> pa_cache_desc:
     """Descriptor of a ``[num_blocks][num_kv_heads][block_size][head_dim]`` pool tensor."""
     if k_cache.dim() != 4:
         raise ValueError("cache must be [num_blocks][num_kv_heads][block_size][head_dim]")
-    nb, hkv, bs, d = (int(x) for x in k_cache.shape)
-    return pa_cache_desc(nb, hkv, bs, d, _dtype_code(k_cache))
+    return pa_cache_desc(*k_cache.shape, _dtype_code(k_cache))
 
 
 def _same_pool(k_cache, v_cache):
@@ -650,10 +649,11 @@ def _rows(t, name: str, dtype):
     _on_current_device(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    n, h, d = (int(x) for x in t.shape)
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if (d > 1 and s2 != 1) or (h > 1 and s1 != d):
         raise ValueError(f"{name} must be contiguous in heads and head_dim")
-    return ctypes.c_void_p(t.data_ptr()), int(t.stride(0)) if n > 1 else h * d
+    return t.data_ptr(), s0 if n > 1 else h * d
 
 
 def _rope_call(entry, scales, q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, rope,
@@ -662,19 +662,20 @@ def _rope_call(entry, scales, q_out, q, k, v, positions, slot_mapping, k_cache, 
     _same_pool(k_cache, v_cache)
     desc = cache_desc(k_cache)
     t = int(slot_mapping.shape[0])
-    if (k.dim() != 3 or tuple(k.shape) != (t, desc.num_kv_heads, desc.head_dim)
-            or k.shape != v.shape):
+    if k.shape != (t, desc.num_kv_heads, desc.head_dim) or k.shape != v.shape:
         raise ValueError("k and v must be [num_tokens][num_kv_heads][head_dim]")
     if q.dim() != 3 or q.shape[0] != t or q.shape[2] != desc.head_dim or q_out.shape != q.shape:
         raise ValueError("q and q_out must be [num_tokens][num_heads][head_dim]")
-    if tuple(positions.shape) != (rope.num_axes, t):
+    if positions.shape != (rope.num_axes, t):
         raise ValueError("positions must be [num_axes][num_tokens]")
     if q_out.dtype != dtype:
         raise TypeError(f"q_out must be {dtype}, got {q_out.dtype}")
     for x in scales:
-        if tuple(x.shape) != (desc.num_kv_heads,):
+        if x.shape != (desc.num_kv_heads,):
             raise ValueError("k_scale and v_scale must be [num_kv_heads]")
-    (qp, qs), (kp, ks), (vp, vs) = (_rows(x, n, dtype) for x, n in ((q, "q"), (k, "k"), (v, "v")))
+    qp, qs = _rows(q, "q", dtype)
+    kp, ks = _rows(k, "k", dtype)
+    vp, vs = _rows(v, "v", dtype)
     _check(entry(
         _dev(q_out, "q_out"), qp, kp, vp, qs, ks, vs, _dev(positions, "positions", torch.int32),
         _dev(slot_mapping, "slot_mapping", torch.int64), t, int(q.shape[1]),

@@ -544,8 +544,9 @@ static int rope_impl(void* q_out, const void* q, const void* k, const void* v, i
         if (rope->axis[i] >= rope->num_axes)
             return fail(PA_ERR_INVALID_ARG, "axis[%d] = %d, num_axes %d", i, rope->axis[i], rope->num_axes);
         // turns per position modulo 1, in units of 2^-64 (64-bit significand)
-        const long double t = (long double)rope->inv_freq[i] / 6.283185307179586476925286766559L;
-        p.turns[i] = (uint64_t)std::min(18446744073709551615.0L, std::floor((t - std::floor(t)) * 0x1p64L));
+        long double t = (long double)rope->inv_freq[i] * 0.15915494309189533576888376337251L;
+        if (t < 0 || t >= 1) t -= std::floor(t);
+        p.turns[i] = (uint64_t)std::min(18446744073709551615.0L, t * 0x1p64L);
         p.axis[i] = rope->axis[i];
     }
     if (num_heads < 0 || num_heads > 65535)

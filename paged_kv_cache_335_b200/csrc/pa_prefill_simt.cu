@@ -7,10 +7,12 @@
 // softmax (Milakov and Gimelshein, "Online normalizer calculation for softmax").
 //
 // CTA = 64 queries of one head against tiles of 64 keys; thread (ty, tx) of
-// 16 x 16 holds a 4 x 4 block of scores and a 4 x D/16 block of the output.
-// Q and K lie transposed in shared memory so that a thread reads its four
-// queries and four keys of one dimension as two 16-byte words per 16 fma. Bound
-// by the fp32 fma rate and the shared-memory reads that feed it.
+// 16 x 16 holds the scores of queries 4 ty .. and keys tx, tx + 16, .. and a 4 x D/16 block
+// of the output. Rows lie as in memory, 4 floats longer in shared memory, so that
+// 16-byte reads along a row are free of bank conflicts, and the next tile's K and V
+// arrive by cp.async meanwhile. The weights of a query pass through shared
+// memory within its warp. Bound by the fp32 fma rate (64 x 64 x D x 2 per tile: 2.2 us of an
+// SM at D = 64) and by the longest prompt's row of tiles.
 #include <math.h>
 
 #include "pa_device.cuh"
@@ -61,18 +63,35 @@ __device__ __forceinline__ void dot_tile(const float* at, const float* bt, int t
     }
 }
 
+// Rows [row0, row0 + 64) x D of a packed tensor by cp.async, `pitch` floats apart in shared
+// memory; rows at or past `end` become zeros.
+template <int D>
+__device__ __forceinline__ void load_async(float* dst, int pitch, const float* src, int64_t stride, int row0,
+                                           int end) {
+    for (int i = threadIdx.x; i < kB * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), c = i % (D / 4);
+        const bool in = row0 + r < end;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                     :: "r"((uint32_t)__cvta_generic_to_shared(dst + r * pitch + 4 * c)),
+                        "l"(src + (int64_t)(in ? row0 + r : 0) * stride + 4 * c), "r"(in ? 16 : 0)
+                     : "memory");
+    }
+}
+
 template <int D>
 constexpr size_t smem_prefill() {
-    return sizeof(float) * (2 * (size_t)D * kPad + (size_t)kB * D);
+    return sizeof(float) * kB * (3 * (size_t)(D + 4) + 2 * (size_t)D + kPad);
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads)
 prefill_simt_kernel(const PrefillParams p) {
     extern __shared__ __align__(16) float sm[];
-    float* qt = sm;                  // [D][kPad]
-    float* kt = qt + D * kPad;       // [D][kPad]; then the weights [key][kPad]
-    float* vs = kt + D * kPad;       // [kB][D]
+    constexpr int kPitch = D + 4;
+    float* qs = sm;                        // [kB][kPitch]
+    float* ks = qs + kB * kPitch;          // [2][kB][kPitch]
+    float* vs = ks + 2 * kB * kPitch;      // [2][kB][D]
+    float* ps = vs + 2 * kB * D;           // [kB][kPad] weights
     const auto tiles = [](int len) { return (len + kB - 1) / kB; };
     PromptWalk walk;
     const PromptTile t = walk.find(p, tiles, blockIdx.x, true);
@@ -85,7 +104,13 @@ prefill_simt_kernel(const PrefillParams p) {
     const float* v = static_cast<const float*>(p.v) + (int64_t)kh * D;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int end = t.start + t.len, q0 = t.tile * kB;
-    load_t<D>(qt, q, p.q_stride, t.start + q0, end);
+    auto load_kv = [&](int buf, int j0) {
+        load_async<D>(ks + buf * kB * kPitch, kPitch, k, p.k_stride, t.start + j0, end);
+        load_async<D>(vs + buf * kB * D, D, v, p.v_stride, t.start + j0, end);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    load_async<D>(qs, kPitch, q, p.q_stride, t.start + q0, end);
+    load_kv(0, 0);
     float o[4][D / 16], m[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -94,26 +119,43 @@ prefill_simt_kernel(const PrefillParams p) {
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) o[i][j] = 0.f;
     }
-    for (int j0 = 0; j0 <= q0; j0 += kB) {
-        __syncthreads();
-        load_t<D>(kt, k, p.k_stride, t.start + j0, end);
-        for (int i = threadIdx.x; i < kB * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), c = i % (D / 4);
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (t.start + j0 + r < end)
-                x = *reinterpret_cast<const float4*>(v + (int64_t)(t.start + j0 + r) * p.v_stride + 4 * c);
-            *reinterpret_cast<float4*>(vs + r * D + 4 * c) = x;
+    for (int j0 = 0, buf = 0; j0 <= q0; j0 += kB, buf ^= 1) {
+        if (j0 + kB <= q0) {
+            load_kv(buf ^ 1, j0 + kB);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
         __syncthreads();
+        const float* kb = ks + buf * kB * kPitch + tx * kPitch;
+        const float* vb = vs + buf * kB * D + 4 * tx;
+        const float* qb = qs + 4 * ty * kPitch;
         float s[4][4];
-        dot_tile<D>(qt, kt, ty, tx, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+        for (int d = 0; d < D; d += 4) {
+            float4 a[4], b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[i] = *reinterpret_cast<const float4*>(qb + i * kPitch + d);
+                b[i] = *reinterpret_cast<const float4*>(kb + 16 * i * kPitch + d);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    s[i][j] = fmaf(a[i].w, b[j].w, fmaf(a[i].z, b[j].z, fmaf(a[i].y, b[j].y, fmaf(a[i].x, b[j].x, s[i][j]))));
+        }
         const bool diag = j0 == q0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float mx = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                s[i][j] = diag && 4 * tx + j > 4 * ty + i ? -INFINITY : s[i][j] * p.scale_log2;
+                s[i][j] = diag && tx + 16 * j > 4 * ty + i ? -INFINITY : s[i][j] * p.scale_log2;
                 mx = fmaxf(mx, s[i][j]);
             }
 #pragma unroll
@@ -127,34 +169,38 @@ prefill_simt_kernel(const PrefillParams p) {
             for (int j = 0; j < 4; ++j) {
                 s[i][j] = exp2f(s[i][j] - mn);
                 sum += s[i][j];
+                ps[(4 * ty + i) * kPad + tx + 16 * j] = s[i][j];
             }
             l[i] = fmaf(l[i], al, sum);
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) o[i][j] *= al;
         }
-        __syncthreads();  // the keys are no longer needed
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<float4*>(kt + (4 * tx + j) * kPad + 4 * ty) =
-                make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
-        __syncthreads();
+        __syncwarp();  // a query's weights come from the 16 lanes of its ty
         // on the diagonal a key past the query is left out, not multiplied by a
         // weight of 0: its value may be infinite or NaN
-#pragma unroll 4
-        for (int c = 0; c < kB; ++c) {
-            const float4 w4 = *reinterpret_cast<const float4*>(kt + c * kPad + 4 * ty);
-            const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll 2
+        for (int c = 0; c < kB; c += 4) {
+            float4 w[4];
 #pragma unroll
-            for (int g = 0; g < D / 64; ++g) {
-                const float4 x4 = *reinterpret_cast<const float4*>(vs + c * D + 64 * g + 4 * tx);
-                const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+            for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(ps + (4 * ty + i) * kPad + c);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+            for (int e = 0; e < 4; ++e) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (!diag || c <= 4 * ty + i) o[i][4 * g + j] = fmaf(w[i], x[j], o[i][4 * g + j]);
+                for (int g = 0; g < D / 64; ++g) {
+                    const float4 x = *reinterpret_cast<const float4*>(vb + (c + e) * D + 64 * g);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (diag && c + e > 4 * ty + i) continue;
+                        const float wi = e == 0 ? w[i].x : e == 1 ? w[i].y : e == 2 ? w[i].z : w[i].w;
+                        o[i][4 * g + 0] = fmaf(wi, x.x, o[i][4 * g + 0]);
+                        o[i][4 * g + 1] = fmaf(wi, x.y, o[i][4 * g + 1]);
+                        o[i][4 * g + 2] = fmaf(wi, x.z, o[i][4 * g + 2]);
+                        o[i][4 * g + 3] = fmaf(wi, x.w, o[i][4 * g + 3]);
+                    }
+                }
             }
         }
+        __syncthreads();  // the buffers are read before the next tile but one
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
