@@ -591,7 +591,8 @@ int pa_prefill(void* out, const void* q, const void* k, const void* v, int64_t q
  *   weights       device, float [num_seqs][num_kv_heads][weights_stride], written
  *                 whole: zeros from the prompt's length on, and for a skipped prompt.
  *   weights_stride  at least max_seq_len.
- * Other arguments and rules as pa_prefill. The sums are fp32 in a fixed order.
+ * Other arguments and rules as pa_prefill. The sums are fp32, in an order that depends on
+ * max_seq_len and last_queries alone: a call repeated gives the same bits.
  */
 int pa_prefill_weights(float* weights, int64_t weights_stride, const void* q, const void* k,
                        int64_t q_stride, int64_t k_stride, const float* lse,

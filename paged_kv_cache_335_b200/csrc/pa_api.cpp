@@ -646,6 +646,7 @@ static int prefill_params(pa::PrefillParams* p, const void* q, const void* k, in
     p->head_dim = head_dim;
     p->last_queries = 0;
     p->split_heads = 0;
+    p->test_skip_position = g_test_skip_position;
     p->scale_log2 = scale * 1.4426950408889634f;
     return PA_OK;
 }

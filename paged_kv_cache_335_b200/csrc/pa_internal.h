@@ -133,6 +133,7 @@ struct PrefillParams {
     int32_t num_seqs, total_tokens, max_seq_len, num_heads, num_kv_heads, head_dim;
     int32_t last_queries;       // pa_prefill_weights: 0 = every query
     int32_t split_heads;        // pa_prefill_weights, set by its launcher
+    int32_t test_skip_position; // -1; >= 0 only under pa_test_skip_load (timeout test)
     float scale_log2;           // softmax scale * log2(e)
 };
 

@@ -453,7 +453,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         uint32_t par_s = 0, par_o = 0;
         bool ok = true;
         for (int n = 0; ok; ++n, leave_item(ib, n - 1)) {
-            if (!wait_item(ib, dead, n)) break;
+            // (the two warps agree on every give-up: one would wait for the other at the barrier)
+            if (pair_any(pair_id, !wait_item(ib, dead, n))) break;
             const int seq = ib.slots[8 * (n % kSlots)];
             if (seq == kEnd) break;
             if (seq < 0) continue;
@@ -730,8 +731,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                                 !(ok = wait_or_dead(dead, b_empty + 8 * (edge2 % S_), (edge2 / S_) & 1)))
                                 break;
                         }
-                        load_tile<D>(ring + at.st * C::kTile, i & 1 ? &vmap : &kmap, it.kh, it.start + j * kBlk,
-                                     b_full + 8 * at.st);
+                        if (loaded != p.test_skip_position)
+                            load_tile<D>(ring + at.st * C::kTile, i & 1 ? &vmap : &kmap, it.kh,
+                                         it.start + j * kBlk, b_full + 8 * at.st);
                         if (edge) {
                             mbar_arrive(b_edge + 8 * (edges & 1));
                             edge2 = edge1;
@@ -925,7 +927,7 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
         bool ok = true;
         for (int n = 0; ok; ++n) {
             Item it = take_item(ib, dead, n);
-            if (it.seq == kEnd) break;
+            if (pair_any(pair_id, it.seq == kEnd)) break;   // (the two warps agree, as on a give-up below)
             if (it.seq < 0) continue;
             const Queries qs(it, p.last_queries);
             const Heads hs(it, p);
@@ -1079,7 +1081,7 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
 #pragma unroll
                     for (int e = 0; e < 4; ++e) lse[at.st * kBlk + 32 * e + lane] = mine[e];
                     __syncwarp();
-                    if (lane == 0)
+                    if (lane == 0 && loaded != p.test_skip_position)
                         load_tile<D>(raw + C::kRing + at.st * C::kTile, &qmap, head0 + h, it.start + qs.q0(qt),
                                      b_full + 8 * at.st);
                     __syncwarp();
