@@ -55,7 +55,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // token of each, and takes kBatch words at a time: with one load per step a row of 32K
 // took 53 us, each step a memory latency. The first digit is sign, exponent and two
 // bits of a heavy-tailed distribution, a few dozen bins: each bin has kCopies places,
-// so that warps collide less.
+// so that a warp's lanes collide less.
 constexpr int kCopies = 4;
 constexpr int kBatch = 8;
 constexpr int kMaxWarps = 32;
@@ -131,8 +131,21 @@ __device__ __forceinline__ int select_row(const float* w, int cand, int edge, ui
     const int wpw = (words + kWarps - 1) / kWarps;
     const int w0 = min(words, warp * wpw), w1 = min(words, w0 + wpw);
     if constexpr (kShared) {
-        each_word<false>(w, keys, w0, w1, cand, [&](int i, uint32_t key, bool) { keys[32 * i + lane] = key; });
-        __syncwarp();   // (a warp reads its own words alone)
+        // four tokens per load where the row is aligned, eight loads of a thread in flight
+        const int quads = (reinterpret_cast<uintptr_t>(w) & 15u) == 0 ? cand / 4 : 0;
+        for (int i0 = tid; i0 < quads; i0 += kBatch * kThreads) {
+            float4 x[kBatch];
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e)
+                if (i0 + e * kThreads < quads) x[e] = __ldg(reinterpret_cast<const float4*>(w) + i0 + e * kThreads);
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e)
+                if (i0 + e * kThreads < quads)
+                    reinterpret_cast<uint4*>(keys)[i0 + e * kThreads] =
+                        make_uint4(weight_key(x[e].x), weight_key(x[e].y), weight_key(x[e].z), weight_key(x[e].w));
+        }
+        for (int t = 4 * quads + tid; t < cand; t += kThreads) keys[t] = weight_key(__ldg(w + t));
+        __syncthreads();
     }
     // The edge-th largest key among the candidates, and how many of the tokens
     // that hold exactly that key are taken (the lowest indices).
@@ -145,7 +158,7 @@ __device__ __forceinline__ int select_row(const float* w, int cand, int edge, ui
             __syncthreads();
             each_word<kShared>(w, keys, w0, w1, cand, [&](int, uint32_t key, bool in) {
                 if (in && (key & known) == prefix)
-                    atomicAdd(&hist[((key >> shift) & mask) * kCopies + (warp & (kCopies - 1))], 1);
+                    atomicAdd(&hist[((key >> shift) & mask) * kCopies + (lane & (kCopies - 1))], 1);
             });
             __syncthreads();
             // bins from the top, kBins / kThreads to a thread: the one that holds rank `want`
@@ -300,7 +313,7 @@ evict_select_kernel(const EvictParams p) {
         }
         __syncthreads();
         // (kPlaced words at a time, their weights in flight together)
-        constexpr int kPlaced = 4;
+        constexpr int kPlaced = 8;
         for (int i0 = warp; 32 * i0 < edge; i0 += kPlaced * kWarps) {
             int src[kPlaced];
             float v[kPlaced];

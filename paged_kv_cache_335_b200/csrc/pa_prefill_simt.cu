@@ -15,6 +15,8 @@
 // SM at D = 64) and by the longest prompt's row of tiles.
 #include <math.h>
 
+#include <type_traits>
+
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pa_prefill_tile.cuh"
@@ -111,13 +113,14 @@ prefill_simt_kernel(const PrefillParams p) {
     };
     load_async<D>(qs, kPitch, q, p.q_stride, t.start + q0, end);
     load_kv(0, 0);
-    float o[4][D / 16], m[4], l[4];
+    float2 o[4][D / 32];
+    float m[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) o[i][j] = 0.f;
+        for (int j = 0; j < D / 32; ++j) o[i][j] = make_float2(0.f, 0.f);
     }
     for (int j0 = 0, buf = 0; j0 <= q0; j0 += kB, buf ^= 1) {
         if (j0 + kB <= q0) {
@@ -130,11 +133,12 @@ prefill_simt_kernel(const PrefillParams p) {
         const float* kb = ks + buf * kB * kPitch + tx * kPitch;
         const float* vb = vs + buf * kB * D + 4 * tx;
         const float* qb = qs + 4 * ty * kPitch;
-        float s[4][4];
+        // sums over even and odd dimensions side by side: two products per instruction
+        float2 s2[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+            for (int j = 0; j < 4; ++j) s2[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
         for (int d = 0; d < D; d += 4) {
             float4 a[4], b[4];
@@ -146,15 +150,19 @@ prefill_simt_kernel(const PrefillParams p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    s[i][j] = fmaf(a[i].w, b[j].w, fmaf(a[i].z, b[j].z, fmaf(a[i].y, b[j].y, fmaf(a[i].x, b[j].x, s[i][j]))));
+                for (int j = 0; j < 4; ++j) {
+                    s2[i][j] = fma2(make_float2(a[i].x, a[i].y), make_float2(b[j].x, b[j].y), s2[i][j]);
+                    s2[i][j] = fma2(make_float2(a[i].z, a[i].w), make_float2(b[j].z, b[j].w), s2[i][j]);
+                }
         }
         const bool diag = j0 == q0;
+        float s[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float mx = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+                s[i][j] = s2[i][j].x + s2[i][j].y;
                 s[i][j] = diag && tx + 16 * j > 4 * ty + i ? -INFINITY : s[i][j] * p.scale_log2;
                 mx = fmaxf(mx, s[i][j]);
             }
@@ -173,33 +181,38 @@ prefill_simt_kernel(const PrefillParams p) {
             }
             l[i] = fmaf(l[i], al, sum);
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) o[i][j] *= al;
+            for (int j = 0; j < D / 32; ++j) o[i][j] = mul2(o[i][j], make_float2(al, al));
         }
         __syncwarp();  // a query's weights come from the 16 lanes of its ty
         // on the diagonal a key past the query is left out, not multiplied by a
         // weight of 0: its value may be infinite or NaN
+        auto add_values = [&](auto on_diagonal) {
 #pragma unroll 2
-        for (int c = 0; c < kB; c += 4) {
-            float4 w[4];
+            for (int c = 0; c < kB; c += 4) {
+                float4 w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(ps + (4 * ty + i) * kPad + c);
+                for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(ps + (4 * ty + i) * kPad + c);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 4; ++e) {
 #pragma unroll
-                for (int g = 0; g < D / 64; ++g) {
-                    const float4 x = *reinterpret_cast<const float4*>(vb + (c + e) * D + 64 * g);
+                    for (int g = 0; g < D / 64; ++g) {
+                        const float4 x = *reinterpret_cast<const float4*>(vb + (c + e) * D + 64 * g);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (diag && c + e > 4 * ty + i) continue;
-                        const float wi = e == 0 ? w[i].x : e == 1 ? w[i].y : e == 2 ? w[i].z : w[i].w;
-                        o[i][4 * g + 0] = fmaf(wi, x.x, o[i][4 * g + 0]);
-                        o[i][4 * g + 1] = fmaf(wi, x.y, o[i][4 * g + 1]);
-                        o[i][4 * g + 2] = fmaf(wi, x.z, o[i][4 * g + 2]);
-                        o[i][4 * g + 3] = fmaf(wi, x.w, o[i][4 * g + 3]);
+                        for (int i = 0; i < 4; ++i) {
+                            if (decltype(on_diagonal)::value && c + e > 4 * ty + i) continue;
+                            const float wi = e == 0 ? w[i].x : e == 1 ? w[i].y : e == 2 ? w[i].z : w[i].w;
+                            const float2 w2 = make_float2(wi, wi);
+                            o[i][2 * g] = fma2(w2, make_float2(x.x, x.y), o[i][2 * g]);
+                            o[i][2 * g + 1] = fma2(w2, make_float2(x.z, x.w), o[i][2 * g + 1]);
+                        }
                     }
                 }
             }
-        }
+        };
+        if (diag)
+            add_values(std::true_type());
+        else
+            add_values(std::false_type());
         __syncthreads();  // the buffers are read before the next tile but one
     }
 #pragma unroll
@@ -213,8 +226,8 @@ prefill_simt_kernel(const PrefillParams p) {
 #pragma unroll
         for (int g = 0; g < D / 64; ++g)
             *reinterpret_cast<float4*>(dst + 64 * g + 4 * tx) =
-                make_float4(o[i][4 * g] * inv, o[i][4 * g + 1] * inv, o[i][4 * g + 2] * inv,
-                            o[i][4 * g + 3] * inv);
+                make_float4(o[i][2 * g].x * inv, o[i][2 * g].y * inv, o[i][2 * g + 1].x * inv,
+                            o[i][2 * g + 1].y * inv);
         if (p.lse != nullptr && tx == 0)
             p.lse[(int64_t)h * p.total_tokens + t.start + row] = (m[i] + log2f(l[i])) * 0.6931471805599453f;
     }
