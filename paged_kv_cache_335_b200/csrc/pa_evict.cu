@@ -480,7 +480,8 @@ evict_shift_kernel(const EvictParams p) {
 // every score (log2 units) and each partition's running max and sum.
 constexpr int kAddThreads = 256;
 constexpr int kAddTokens = 4;  // per thread, consecutive: one 16-byte load per head
-constexpr int kMaxHeads = 32;  // of a group, per round
+constexpr int kMaxHeads = 8;   // of a group, per round: their scores are on the way while the warps
+                               // (one per head) form the log-sum-exps
 
 __global__ void __launch_bounds__(kAddThreads)
 add_weights_kernel(const AddWeightsParams p) {
@@ -493,9 +494,15 @@ add_weights_kernel(const AddWeightsParams p) {
     const int t = (blockIdx.x * kAddThreads + threadIdx.x) * kAddTokens;
     const int group = p.num_heads / p.num_kv_heads;
     const int parts = (n + p.partition_size - 1) / p.partition_size;
+    float* w = p.weights + ((int64_t)s * p.num_kv_heads + kh) * p.weights_stride + t;
     float acc[kAddTokens] = {0.f, 0.f, 0.f, 0.f};
     for (int h0 = 0; h0 < group; h0 += kMaxHeads) {
         const int heads = min(kMaxHeads, group - h0);
+        const float* sc = p.scores + ((int64_t)s * p.num_heads + kh * group + h0) * p.score_stride + t;
+        float4 x[kMaxHeads];
+#pragma unroll
+        for (int h = 0; h < kMaxHeads; ++h)
+            if (h < heads && t < n) x[h] = __ldcs(reinterpret_cast<const float4*>(sc + (int64_t)h * p.score_stride));
         for (int h = warp; h < heads; h += kAddThreads / 32) {
             const float2* ml = reinterpret_cast<const float2*>(p.ml) +
                                ((int64_t)s * p.num_heads + kh * group + h0 + h) * p.num_partitions;
@@ -511,23 +518,19 @@ add_weights_kernel(const AddWeightsParams p) {
             if (lane == 0) lse[h] = L == 0.f ? INFINITY : M + log2f(L);
         }
         __syncthreads();
-        if (t < n) {
-            const float* sc = p.scores + ((int64_t)s * p.num_heads + kh * group + h0) * p.score_stride + t;
-#pragma unroll 8
-            for (int h = 0; h < heads; ++h) {
-                const float4 x = __ldcs(reinterpret_cast<const float4*>(sc + (int64_t)h * p.score_stride));
-                const float e = lse[h];
-                acc[0] += exp2f(x.x - e);
-                acc[1] += exp2f(x.y - e);
-                acc[2] += exp2f(x.z - e);
-                acc[3] += exp2f(x.w - e);
-            }
+#pragma unroll
+        for (int h = 0; h < kMaxHeads; ++h) {
+            if (h >= heads || t >= n) break;
+            const float e = lse[h];
+            acc[0] += exp2f(x[h].x - e);
+            acc[1] += exp2f(x[h].y - e);
+            acc[2] += exp2f(x[h].z - e);
+            acc[3] += exp2f(x[h].w - e);
         }
         __syncthreads();
     }
-    float* w = p.weights + ((int64_t)s * p.num_kv_heads + kh) * p.weights_stride + t;
     if (t + kAddTokens <= n && (reinterpret_cast<uintptr_t>(w) & 15u) == 0) {
-        float4 x = *reinterpret_cast<float4*>(w);
+        float4 x = *reinterpret_cast<const float4*>(w);
         x.x += acc[0];
         x.y += acc[1];
         x.z += acc[2];

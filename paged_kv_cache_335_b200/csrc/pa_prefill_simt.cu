@@ -15,6 +15,7 @@
 // SM at D = 64) and by the longest prompt's row of tiles.
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "pa_device.cuh"
@@ -96,8 +97,8 @@ prefill_simt_kernel(const PrefillParams p) {
     float* ps = vs + 2 * kB * D;           // [kB][kPad] weights
     const auto tiles = [](int len) { return (len + kB - 1) / kB; };
     PromptWalk walk;
-    const PromptTile t = walk.find(p, tiles, blockIdx.x, true);
-    const int h = blockIdx.y;
+    const PromptTile t = walk.find(p, tiles, blockIdx.x / p.num_heads, true);
+    const int h = blockIdx.x % p.num_heads;
     if (walk.bad && h == 0) atomicOr(&s_status_prefill_simt, kStatusBadIndex);
     if (t.seq < 0) return;
     const int kh = h / (p.num_heads / p.num_kv_heads);
@@ -245,8 +246,8 @@ prefill_weights_simt_kernel(const PrefillParams p) {
     float* lq = qt + D * kPad;       // [kB] log-sum-exp of the queries, log2 units
     const auto tiles = [](int len) { return (len + kB - 1) / kB; };
     PromptWalk walk;
-    const PromptTile t = walk.find(p, tiles, blockIdx.x, false);
-    const int kh = blockIdx.y;
+    const PromptTile t = walk.find(p, tiles, blockIdx.x / p.num_kv_heads, false);
+    const int kh = blockIdx.x % p.num_kv_heads;
     if (walk.bad && kh == 0) atomicOr(&s_status_prefill_simt, kStatusBadIndex);
     if (t.seq < 0) return;
     const int group = p.num_heads / p.num_kv_heads;
@@ -296,13 +297,18 @@ prefill_weights_simt_kernel(const PrefillParams p) {
 
 template <int D>
 cudaError_t launch_prefill_t(const PrefillParams& p, cudaStream_t stream) {
-    constexpr size_t smem = smem_prefill<D>();
+    // one more than there can be tiles: its CTAs look every prompt over
+    const int64_t ctas = ((int64_t)(p.total_tokens / kB) + p.num_seqs + 1) * p.num_heads;
+    if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+    // Two CTAs share an SM at D = 64 (more work in flight: 536 CTAs take 148 us, one at a time
+    // 156). With no more than two per SM in all, the longest tile's time is the kernel's, and it
+    // is shorter alone, the others queueing for the SMs that finish (280 CTAs: 77 us
+    // against 92): more shared memory than half an SM's keeps a second one away.
+    const size_t smem = ctas <= 2 * 148 ? std::max(smem_prefill<D>(), (size_t)120 * 1024) : smem_prefill<D>();
     cudaError_t e = cudaFuncSetAttribute(prefill_simt_kernel<D>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    // one more than there can be tiles: its CTAs look every prompt over
-    const dim3 grid((unsigned)(p.total_tokens / kB + p.num_seqs + 1), (unsigned)p.num_heads);
-    prefill_simt_kernel<D><<<grid, kThreads, smem, stream>>>(p);
+    prefill_simt_kernel<D><<<(unsigned)ctas, kThreads, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -313,8 +319,9 @@ cudaError_t launch_weights_t(const PrefillParams& p, cudaStream_t stream) {
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     // one more than there can be tiles: its CTAs look every prompt over
-    const dim3 grid((unsigned)(p.total_tokens / kB + p.num_seqs + 1), (unsigned)p.num_kv_heads);
-    prefill_weights_simt_kernel<D><<<grid, kThreads, smem, stream>>>(p);
+    const int64_t ctas = ((int64_t)(p.total_tokens / kB) + p.num_seqs + 1) * p.num_kv_heads;
+    if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+    prefill_weights_simt_kernel<D><<<(unsigned)ctas, kThreads, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
