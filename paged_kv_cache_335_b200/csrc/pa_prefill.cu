@@ -16,10 +16,10 @@
 //   warp 17: loads Q and the ring of K and V tiles by TMA, and finds the next item;
 //   warps 0..7 and 8..15: the softmax of row blocks 0 and 1, two threads per row (of warps
 //     that share TMEM lanes), which exchange the row's maximum in every tile and its sum at
-//     the end. P (bf16) overwrites the first half of each thread's scores in TMEM, which are
-//     read twice (for the maximum, then for the weights): kept in registers, they
-//     left the rest of the loop to local memory, and with shared memory taking all of
-//     the L1 cache each of those loads is an L2 access;
+//     the end. The scores are read twice (for the maximum, then for the weights): kept in
+//     registers, they left the rest of the loop to local memory, and with shared
+//     memory taking all of the L1 cache each of those loads is an L2 access. P (bf16)
+//     overwrites the first half of each thread's scores in TMEM, or has its own columns;
 //   warps 18 and 19: on the tiles that the diagonal crosses, zero the elements of V that are
 //     not finite, and the rows behind the prompt, before the tensor core reads
 //     them: a masked weight is 0, and 0 x infinity would not be. The epilogue adds the
@@ -32,19 +32,23 @@
 //
 // Weights. weights[t] = sum over heads of the group and queries i >= t of
 // 2^(score - lse_i): S^T = K Q^T with the keys as rows, so that a key's sum stays in one
-// thread (two: one per half of the queries' columns); query tiles stream past two key tiles (one would read each from L2 twice as
-// often, which bounded it: 0.77 us per 128 x 128 scores and SM). A part of the
-// exponentials runs on the fp32 units.
+// thread (two: one per half of the queries' columns, four per SM sub-partition, which hide
+// more of each other's waits than two: 873 -> 665 us at 8K under 64/8 heads); query tiles
+// stream past two key tiles, so that each is read from L2 half as often.
 //
 // Both kernels stay on their SM and take item after item: the grid is one CTA per item, and a
 // running CTA cancels the launch of one that has not started and does its work
 // (cluster launch control), so that the next item's tiles load while this one's
 // epilogue runs, and long and short prompts balance without a counter in memory.
 //
-// Bound by the tensor cores (64 cycles per 128 x 128 x 16 product: 1024 per key tile and
-// row block at head_dim 128), the exponential unit (16 per cycle and SM: 1024 cycles per
-// 128 x 128 weights) and, in between, by the chain S -> softmax -> P V -> next S of a row
-// block, which the other row block only partly covers.
+// Bounds of the attention: the tensor cores (64 cycles per 128 x 128 x 16 product: 1024 per
+// key tile and row block at head_dim 128), the exponential unit (16 per cycle and SM:
+// 1024 cycles per 128 x 128 weights) and, in between, the chain S -> softmax -> P V ->
+// next S of a row block (about 1500 + 512 + 512 + 380 cycles), which the other row
+// block only partly covers. 16K tokens of 64/8 heads: 3.46 ms = 1270 TFLOP/s in a row of
+// five (power-capped clock), tensor pipe 54% active at 4K. A product of 64 keys costs the
+// cycles of one of 128, so smaller steps with two score buffers were slower (4.4 ms).
+// Bound of the weights: the exponential unit (73% active at 4K).
 #include <math.h>
 
 #include <algorithm>
@@ -323,10 +327,16 @@ struct AttnCfg {
     static constexpr int kXch = kRing + kStages * kTile;
     static constexpr int kItems = kXch + 4 * kBlk * 4;
     static constexpr int kBars = kItems + kItemBytes;
-    // q 2, its release 2, full S, empty S, s 2, p 2, o 2, note 2, edge 2, clean 2, fin
-    static constexpr int kNumBars = 2 * kStages + 17 + kItemBars;
+    // q 2, its release 2, full S, empty S, s 2, p 2, pv 2, o 2, note 2, edge 2, clean 2, fin
+    static constexpr int kNumBars = 2 * kStages + 19 + kItemBars;
     static constexpr int kSmem = kBars + 8 * kNumBars + 32;   // + TMEM slot, dead, taken 4, noted 2
     static constexpr uint32_t kColO = 256;
+    // At head_dim 64 TMEM has room for P beside S (at 128 P overwrites its thread's scores), and
+    // the next scores need not wait for P V: their product goes first.
+    static constexpr bool kOwnP = D == 64;
+    __host__ __device__ static constexpr uint32_t col_p(int b, int half) {
+        return kOwnP ? 384 + 64 * b + 32 * half : kBlk * b + 64 * half;
+    }
     static constexpr uint32_t kIdescQK = umma_idesc(kBlk, kBlk, false);
     static constexpr uint32_t kIdescPV = umma_idesc(kBlk, D, true);
     static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
@@ -380,7 +390,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     }
     const uint32_t bars = smem_u32(smem + C::kBars);
     const uint32_t b_q = bars, b_qfree = b_q + 16, b_full = b_qfree + 16, b_empty = b_full + 8 * S_,
-                   b_s = b_empty + 8 * S_, b_p = b_s + 16, b_o = b_p + 16, b_note = b_o + 16,
+                   b_s = b_empty + 8 * S_, b_p = b_s + 16, b_pv = b_p + 16, b_o = b_pv + 16, b_note = b_o + 16,
                    b_edge = b_note + 16, b_clean = b_edge + 16, b_fin = b_clean + 16;
     const ItemBars ib = item_bars(b_fin + 8, smem + C::kItems, kSoftWarps + 1 + kCleaners);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBars + 8 * C::kNumBars);
@@ -398,6 +408,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             mbar_init(b_qfree + 8 * i, 1);
             mbar_init(b_s + 8 * i, 1);
             mbar_init(b_p + 8 * i, kSoftWarps / 2);
+            mbar_init(b_pv + 8 * i, 1);
             mbar_init(b_o + 8 * i, 1);
             mbar_init(b_note + 8 * i, 1);
             mbar_init(b_edge + 8 * i, 1);
@@ -420,6 +431,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         const int b = warp >> 3, half = (warp >> 2) & 1, row = threadIdx.x & 127;
         const int pair_id = 1 + 4 * b + (warp & 3);
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t tp = tm + lanes + C::col_p(b, half);
         const uint32_t ts = tm + lanes + kBlk * b + 64 * half, to = tm + lanes + C::kColO + D * b + D / 2 * half;
         float* xch = reinterpret_cast<float*>(smem + C::kXch) + 2 * kBlk * b + row;
         // (its sign is in the product; not 0, so that a masked -infinity stays one)
@@ -474,7 +486,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 } else {
                     const bool move = (mt - m) * sl > kRescaleLog2;
                     if (__any_sync(0xffffffffu, move)) {
-                        // S_b's commit came after the last PV of this row block: O is at rest
+                        // O is at rest: S_b's commit came after the last PV of this row block, or
+                        // that is waited for
+                        if (C::kOwnP) wait(b_pv + 8 * b, par_s ^ 1);
+                        tc_fence_after();
                         const float al = move ? ex2((m - mt) * sl) : 1.f;
                         if (move) {
                             m = mt;
@@ -506,7 +521,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                         w[c] = bf16x2(x.x, x.y);
                         sum[c & 1] = add2(sum[c & 1], x);
                     }
-                    tmem_st16_issue(ts + 16 * g, w);
+                    if (C::kOwnP && g == 0) {  // the last P is no longer read (at the first: parity of no use)
+                        wait(b_pv + 8 * b, par_s ^ 1);
+                        tc_fence_after();
+                    }
+                    tmem_st16_issue(tp + 16 * g, w);
                 }
                 tmem_wait_st();
                 l2 = add2(l2, add2(sum[0], sum[1]));
@@ -638,11 +657,19 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                     tc_fence_after();
                     const uint32_t lo = v_lo(ring + pv.st * C::kTile);
                     const bool last = j == k.last(b);
+                    auto next_scores = [&] {
+                        if (last) return;
+                        if (!have_k && !(ok = wait(b_full + 8 * pk.st, pk.par))) return;
+                        have_k = true;
+                        qk(b, pk.st, j + 1 == k.last(b));
+                    };
+                    if (C::kOwnP) next_scores();
                     if (one) {
 #pragma unroll
                         for (int i = 0; i < kBlk / 16; ++i)
-                            umma_ts_words(tm + C::kColO + D * b, tm + kBlk * b + 8 * i + (i < 4 ? 0 : 32), lo + 128 * i,
+                            umma_ts_words(tm + C::kColO + D * b, tm + C::col_p(b, i >> 2) + 8 * (i & 3), lo + 128 * i,
                                           kDescHi, C::kIdescPV, i > 0 || j > 0);
+                        if (C::kOwnP) umma_commit(b_pv + 8 * b);
                         if (last) {
                             umma_commit(b_o + 8 * b);
                             noted[b] = note;
@@ -650,13 +677,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                         }
                     }
                     __syncwarp();
-                    if (!last) {
-                        if (!have_k) {
-                            if (!(ok = wait(b_full + 8 * pk.st, pk.par))) continue;
-                            have_k = true;
-                        }
-                        qk(b, pk.st, j + 1 == k.last(b));
-                    }
+                    if (!C::kOwnP) next_scores();
                 }
                 if (ok && one) {
                     umma_commit(b_empty + 8 * pv.st);
