@@ -46,6 +46,116 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 // ---------------------------------------------------------------------------
+// fill and shift
+// ---------------------------------------------------------------------------
+// Row (token position t of sequence s, kv head kh) of the pools in 16-byte
+// vectors; -1 for a block id outside the pool.
+__device__ __forceinline__ int64_t row_of(const EvictParams& p, int s, int kh, int t) {
+    const int32_t b = __ldg(p.block_tables + (int64_t)s * p.table_stride + (t >> p.log2_block_size));
+    if ((unsigned)b >= (unsigned)p.num_blocks) {
+        atomicOr(&s_status_evict, kStatusBadIndex);
+        return -1;
+    }
+    return (((int64_t)b * p.num_kv_heads + kh) * p.block_size + (t & (p.block_size - 1))) * p.row_vecs;
+}
+
+// Rows into the holes below edge. A warp takes 32 slots, and moves the rows of
+// those that change, 32 / row_vecs rows (of K and of V) per step.
+constexpr int kFillWarps = 8;
+__device__ __forceinline__ void fill_rows(const EvictParams& p, int s, int kh, int j, int edge) {
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)s * p.num_kv_heads + kh;
+    int64_t src = -1, dst = -1;
+    if (j < edge) {
+        const int from = p.kept[row * p.budget + j];
+        if (from != j) {
+            src = row_of(p, s, kh, from);
+            dst = row_of(p, s, kh, j);
+            if (src < 0 || dst < 0) src = dst = -1;
+        }
+    }
+    uint32_t todo = __ballot_sync(0xffffffffu, dst >= 0);
+    const int rows = 32 / p.row_vecs, sub = lane / p.row_vecs, c = lane % p.row_vecs;
+    constexpr int kU = 4;
+    while (todo) {
+        uint4 kv[kU], vv[kU];
+        int64_t d[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            int mine = -1;
+            for (int r = 0; r < rows && todo; ++r) {
+                const int b = __ffs(todo) - 1;
+                todo &= todo - 1;
+                if (r == sub) mine = b;
+            }
+            const int64_t a = __shfl_sync(0xffffffffu, src, mine < 0 ? 0 : mine);
+            d[u] = __shfl_sync(0xffffffffu, dst, mine < 0 ? 0 : mine);
+            if (mine < 0) d[u] = -1;
+            if (d[u] >= 0) {
+                kv[u] = ld_v4(p.k_cache + a + c);
+                vv[u] = ld_v4(p.v_cache + a + c);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+            if (d[u] >= 0) {
+                p.k_cache[d[u] + c] = kv[u];
+                p.v_cache[d[u] + c] = vv[u];
+            }
+    }
+}
+
+__global__ void __launch_bounds__(kFillWarps * 32)
+evict_fill_kernel(const EvictParams p) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int kh = blockIdx.y, s = blockIdx.z;
+    const int n = clamp_len(__ldg(p.context_lens + s), p.max_context_len, false);
+    if (n > p.budget)
+        fill_rows(p, s, kh, blockIdx.x * kFillWarps * 32 + threadIdx.x, p.budget - p.recent);
+}
+
+// The recent rows: slot edge + i gets position n - recent + i. One CTA per
+// (K or V, kv head, sequence) goes through them in ascending chunks that are read whole
+// before any is written: a slot written by a chunk is the source of no later one.
+constexpr int kShiftThreads = 512;
+constexpr int kShiftU = 8;
+template <int kThreads>
+__device__ __forceinline__ void shift_rows(const EvictParams& p, uint4* cache, int s, int kh, int n, int edge) {
+    const int c = threadIdx.x % p.row_vecs, r0 = threadIdx.x / p.row_vecs;
+    const int rows = kThreads / p.row_vecs;  // per pass
+    for (int base = 0; base < p.recent; base += rows * kShiftU) {
+        uint4 v[kShiftU];
+        int64_t d[kShiftU];
+#pragma unroll
+        for (int u = 0; u < kShiftU; ++u) {
+            const int i = base + u * rows + r0;
+            d[u] = -1;
+            if (i < p.recent) {
+                const int64_t a = row_of(p, s, kh, n - p.recent + i);
+                d[u] = row_of(p, s, kh, edge + i);
+                if (a < 0) d[u] = -1;
+                if (d[u] >= 0) v[u] = ld_v4(cache + a + c);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kShiftU; ++u)
+            if (d[u] >= 0) cache[d[u] + c] = v[u];
+        __syncthreads();
+    }
+}
+
+__global__ void __launch_bounds__(kShiftThreads)
+evict_shift_kernel(const EvictParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int kh = blockIdx.y, s = blockIdx.z;
+    const int n = clamp_len(__ldg(p.context_lens + s), p.max_context_len, false);
+    if (n > p.budget)
+        shift_rows<kShiftThreads>(p, blockIdx.x ? p.v_cache : p.k_cache, s, kh, n, p.budget - p.recent);
+}
+
+// ---------------------------------------------------------------------------
 // select
 // ---------------------------------------------------------------------------
 // The threshold key is found digit by digit (11, 11 and 10 bits; four of 8 in short contexts,
@@ -270,8 +380,9 @@ __device__ __forceinline__ int select_row(const float* w, int cand, int edge, ui
     return num_holes;
 }
 
-template <int kThreads, bool kShared>
-__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 5 : 1)
+// kMove: also the rows (else evict_fill_kernel and evict_shift_kernel follow).
+template <int kThreads, bool kShared, bool kMove>
+__global__ void __launch_bounds__(kThreads, kThreads != 256 ? 1 : kMove ? 4 : 5)
 evict_select_kernel(const EvictParams p) {
     constexpr int kWarps = kThreads / 32, kListCap = Select<kThreads>::kListCap;
     extern __shared__ __align__(16) uint32_t sm_u[];
@@ -365,110 +476,12 @@ evict_select_kernel(const EvictParams p) {
         __syncthreads();
     }
     for (int64_t j = p.budget + tid; j < p.weights_stride; j += kThreads) wo[j] = 0.f;
-}
-
-// ---------------------------------------------------------------------------
-// fill and shift
-// ---------------------------------------------------------------------------
-// Row (token position t of sequence s, kv head kh) of the pools in 16-byte
-// vectors; -1 for a block id outside the pool.
-__device__ __forceinline__ int64_t row_of(const EvictParams& p, int s, int kh, int t) {
-    const int32_t b = __ldg(p.block_tables + (int64_t)s * p.table_stride + (t >> p.log2_block_size));
-    if ((unsigned)b >= (unsigned)p.num_blocks) {
-        atomicOr(&s_status_evict, kStatusBadIndex);
-        return -1;
-    }
-    return (((int64_t)b * p.num_kv_heads + kh) * p.block_size + (t & (p.block_size - 1))) * p.row_vecs;
-}
-
-// Rows into the holes below edge. A warp takes 32 slots, and moves the rows of
-// those that change, 32 / row_vecs rows (of K and of V) per step.
-constexpr int kFillWarps = 8;
-__global__ void __launch_bounds__(kFillWarps * 32)
-evict_fill_kernel(const EvictParams p) {
-    asm volatile("griddepcontrol.launch_dependents;");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int kh = blockIdx.y, s = blockIdx.z;
-    const int lane = threadIdx.x & 31;
-    const int edge = p.budget - p.recent;
-    const int n = clamp_len(__ldg(p.context_lens + s), p.max_context_len, false);
-    if (n <= p.budget) return;
-    const int j = (blockIdx.x * kFillWarps + (threadIdx.x >> 5)) * 32 + lane;
-    const int64_t row = (int64_t)s * p.num_kv_heads + kh;
-    int64_t src = -1, dst = -1;
-    if (j < edge) {
-        const int from = p.kept[row * p.budget + j];
-        if (from != j) {
-            src = row_of(p, s, kh, from);
-            dst = row_of(p, s, kh, j);
-            if (src < 0 || dst < 0) src = dst = -1;
-        }
-    }
-    uint32_t todo = __ballot_sync(0xffffffffu, dst >= 0);
-    const int rows = 32 / p.row_vecs, sub = lane / p.row_vecs, c = lane % p.row_vecs;
-    constexpr int kU = 4;
-    while (todo) {
-        uint4 kv[kU], vv[kU];
-        int64_t d[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            int mine = -1;
-            for (int r = 0; r < rows && todo; ++r) {
-                const int b = __ffs(todo) - 1;
-                todo &= todo - 1;
-                if (r == sub) mine = b;
-            }
-            const int64_t a = __shfl_sync(0xffffffffu, src, mine < 0 ? 0 : mine);
-            d[u] = __shfl_sync(0xffffffffu, dst, mine < 0 ? 0 : mine);
-            if (mine < 0) d[u] = -1;
-            if (d[u] >= 0) {
-                kv[u] = ld_v4(p.k_cache + a + c);
-                vv[u] = ld_v4(p.v_cache + a + c);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kU; ++u)
-            if (d[u] >= 0) {
-                p.k_cache[d[u] + c] = kv[u];
-                p.v_cache[d[u] + c] = vv[u];
-            }
-    }
-}
-
-// The recent rows: slot edge + i gets position n - recent + i. One CTA per
-// (K or V, kv head, sequence) goes through them in ascending chunks that are read whole
-// before any is written: a slot written by a chunk is the source of no later one.
-constexpr int kShiftThreads = 512;
-constexpr int kShiftU = 8;
-__global__ void __launch_bounds__(kShiftThreads)
-evict_shift_kernel(const EvictParams p) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int kh = blockIdx.y, s = blockIdx.z;
-    const int n = clamp_len(__ldg(p.context_lens + s), p.max_context_len, false);
-    if (n <= p.budget) return;
-    const int edge = p.budget - p.recent;
-    uint4* cache = blockIdx.x ? p.v_cache : p.k_cache;
-    const int c = threadIdx.x % p.row_vecs, r0 = threadIdx.x / p.row_vecs;
-    const int rows = kShiftThreads / p.row_vecs;  // per pass
-    for (int base = 0; base < p.recent; base += rows * kShiftU) {
-        uint4 v[kShiftU];
-        int64_t d[kShiftU];
-#pragma unroll
-        for (int u = 0; u < kShiftU; ++u) {
-            const int i = base + u * rows + r0;
-            d[u] = -1;
-            if (i < p.recent) {
-                const int64_t a = row_of(p, s, kh, n - p.recent + i);
-                d[u] = row_of(p, s, kh, edge + i);
-                if (a < 0) d[u] = -1;
-                if (d[u] >= 0) v[u] = ld_v4(cache + a + c);
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < kShiftU; ++u)
-            if (d[u] >= 0) cache[d[u] + c] = v[u];
-        __syncthreads();
+    if constexpr (kMove) {
+        __syncthreads();   // `kept` is written
+        for (int j = tid - lane; j < edge; j += kThreads) fill_rows(p, s, kh, j + lane, edge);
+        __syncthreads();   // the fill reads rows behind edge before the shift writes them
+        shift_rows<kThreads>(p, p.k_cache, s, kh, n, edge);
+        shift_rows<kThreads>(p, p.v_cache, s, kh, n, edge);
     }
 }
 
@@ -570,24 +583,28 @@ static cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t sme
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <int kThreads, bool kShared>
+template <int kThreads, bool kShared, bool kMove>
 static cudaError_t launch_select(const EvictParams& p, cudaStream_t stream) {
     const size_t smem = evict_smem_bytes<kThreads>(p.max_context_len, kShared);
-    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<kThreads, kShared>,
+    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<kThreads, kShared, kMove>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    evict_select_kernel<kThreads, kShared>
+    evict_select_kernel<kThreads, kShared, kMove>
         <<<dim3((unsigned)p.num_kv_heads, (unsigned)p.num_seqs), kThreads, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
     const dim3 rows((unsigned)p.num_kv_heads, (unsigned)p.num_seqs);
-    // a row of a short context is bound by its barriers: fewer threads, more rows per SM
-    cudaError_t e = p.max_context_len <= 4096 ? launch_select<256, true>(p, stream)
+    // A row of a short context is bound by its barriers: fewer threads, more rows per SM. Where such
+    // rows fill the SMs, each also moves its own keys and values: 16 x 40 rows of 2064
+    // tokens take 19.7 us on the device, with the two further launches 20.5 and 4 us more of host time.
+    if (p.max_context_len <= 4096 && (int64_t)rows.x * rows.y >= 148)
+        return launch_select<256, true, true>(p, stream);
+    cudaError_t e = p.max_context_len <= 4096 ? launch_select<256, true, false>(p, stream)
                     : evict_smem_bytes<1024>(p.max_context_len, true) <= 227 * 1024
-                        ? launch_select<1024, true>(p, stream)
-                        : launch_select<1024, false>(p, stream);
+                        ? launch_select<1024, true, false>(p, stream)
+                        : launch_select<1024, false, false>(p, stream);
     if (e != cudaSuccess) return e;
     if (p.max_context_len <= p.budget) return cudaSuccess;  // no sequence is over its budget
     const int edge = p.budget - p.recent;

@@ -103,7 +103,7 @@ def test_decode_weights_skips_bad_blocks():
 
 
 @pytest.mark.parametrize("dtype,d,hkv,bs", [(BF16, 128, 3, 16), (F32, 64, 2, 32), (FP8, 64, 5, 16), (I8, 128, 1, 64),
-                                            (F32, 128, 2, 16), (BF16, 64, 4, 256)])
+                                            (F32, 128, 2, 16), (BF16, 64, 4, 256), (BF16, 64, 24, 16), (I8, 64, 23, 32)])
 @pytest.mark.parametrize("budget,recent", [(1, 0), (1, 1), (32, 0), (33, 32), (100, 7), (320, 64), (333, 333),
                                            (699, 20), (1000, 10)])
 def test_evict(dtype, d, hkv, bs, budget, recent):
