@@ -118,3 +118,75 @@ def test_prompt_decode_evict_decode(dtype):
             got = o[s, kh * (h // hkv):(kh + 1) * (h // hkv)].double()
             tol = P.attention_bound(ref, mag, sabs, d, n, dtype)
             assert bool(((got - ref).abs() <= tol).all())
+
+
+def _step_state(seed, dtype=torch.bfloat16):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    s, h, hkv, d, bs = 5, 16, 2, 128, 16
+    kc, vc = (torch.randn((160, hkv, bs, d), generator=g, device=DEV).to(dtype) for _ in range(2))
+    qkv = torch.randn((s, h + 2 * hkv, d), generator=g, device=DEV).to(dtype)
+    tables = torch.randperm(160, generator=g, device=DEV)[:s * 30].reshape(s, 30).int()
+    ctx = torch.tensor([401, 17, 450, 300, 64], dtype=torch.int32, device=DEV)
+    slots = (tables.gather(1, ((ctx - 1) // bs).long()[:, None])[:, 0] * bs + (ctx - 1) % bs).long()
+    st = dict(kc=kc, vc=vc, qkv=qkv, tables=tables, ctx=ctx, slots=slots, pos=(ctx - 1)[None].repeat(3, 1).contiguous(),
+              q=torch.empty((s, h, d), device=DEV, dtype=dtype), out=torch.empty((s, h, d), device=DEV, dtype=dtype),
+              w=torch.rand((s, hkv, 480), generator=g, device=DEV), new=torch.zeros_like(ctx),
+              kept=torch.zeros((s, hkv, 256), dtype=torch.int32, device=DEV))
+    st["ws"] = torch.empty(pa.pa_decode_weights_workspace_size(s, h, 480, kc), dtype=torch.uint8, device=DEV)
+    return st
+
+
+def _step(st, stream=None):
+    q, k, v = st["qkv"][:, :16], st["qkv"][:, 16:18], st["qkv"][:, 18:]
+    pa.pa_rope_append(st["q"], q, k, v, st["pos"], st["slots"], st["kc"], st["vc"],
+                      pa.rope_desc(128, sections=[32, 16, 16]), stream=stream)
+    pa.pa_decode_weights(st["out"], st["w"], st["q"], st["kc"], st["vc"], st["tables"], st["ctx"], 0.09,
+                         max_context_len=480, workspace=st["ws"], stream=stream)
+    pa.pa_evict(st["kc"], st["vc"], st["tables"], st["ctx"], st["w"], st["w"], st["new"], st["kept"], 256, 40,
+                max_context_len=480, stream=stream)
+
+
+def _same(a, b):
+    return all(torch.equal(a[k], b[k]) for k in ("kc", "vc", "q", "out", "w", "new", "kept"))
+
+
+def test_captured_step_replays_with_new_inputs():
+    want = _step_state(32)
+    _step(want)
+    st = _step_state(31)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _step(st)
+    for k, v in _step_state(32).items():
+        st[k].copy_(v)
+    graph.replay()
+    torch.cuda.synchronize()
+    pa.pa_sync_check()
+    assert _same(st, want)
+
+
+def test_two_steps_at_once():
+    """Two streams with states and workspaces of their own, and prompts beside them."""
+    want = [_step_state(s) for s in (33, 34)]
+    for st in want:
+        _step(st)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    q, k, v = (torch.randn((700, h, 64), generator=g, device=DEV).bfloat16() for h in (6, 2, 2))
+    cu = torch.tensor([0, 300, 700], dtype=torch.int32, device=DEV)
+    ref, ref_l, ref_w = torch.empty_like(q), torch.empty((6, 700), device=DEV), torch.empty((2, 2, 400), device=DEV)
+    pa.pa_prefill(ref, q, k, v, cu, 0.125, max_seq_len=400, lse=ref_l)
+    pa.pa_prefill_weights(ref_w, q, k, ref_l, cu, 0.125, max_seq_len=400)
+    sts = [_step_state(s) for s in (33, 34)]
+    outs = [[torch.empty_like(x) for x in (ref, ref_l, ref_w)] for _ in sts]
+    streams = [torch.cuda.Stream() for _ in sts]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for st, o, stream in zip(sts, outs, streams):
+            pa.pa_prefill(o[0], q, k, v, cu, 0.125, max_seq_len=400, lse=o[1], stream=stream)
+            pa.pa_prefill_weights(o[2], q, k, o[1], cu, 0.125, max_seq_len=400, stream=stream)
+    for st, stream in zip(sts, streams):
+        _step(st, stream=stream)
+    torch.cuda.synchronize()
+    pa.pa_sync_check()
+    assert all(_same(a, b) for a, b in zip(sts, want))
+    assert all(torch.equal(a, b) for o in outs for a, b in zip(o, (ref, ref_l, ref_w)))
