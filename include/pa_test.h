@@ -5,10 +5,10 @@
  * and bf16 pa_prefill_weights call (from any thread) leaves ring position `position`
  * of each CTA's pipeline (K/V tiles; query tiles in pa_prefill_weights) unloaded. The
  * consumer waiting for that position gives up after its bounded wait (about one
- * second), the producer and the other waiters then give up in turn, the kernel still terminates, its outputs are invalid, and pa_sync_check
- * returns PA_ERR_TIMEOUT; the CUDA context stays usable. -1 restores normal
- * operation. It exists only so that the timeout path can be tested without a
- * fault or a hang.
+ * second), the producer and the other waiters then give up in turn, the kernel
+ * still terminates, its outputs are invalid, and pa_sync_check returns
+ * PA_ERR_TIMEOUT; the CUDA context stays usable. -1 restores normal operation. It
+ * exists only so that the timeout path can be tested without a fault or a hang.
  *
  * pa_test_last_decode_kernel — which decode kernel the calling thread's last
  * successful pa_decode / pa_decode_grouped / pa_decode_noalloc enqueued:

@@ -46,7 +46,7 @@
 // 1024 cycles per 128 x 128 weights) and, in between, the chain S -> softmax -> P V ->
 // next S of a row block (about 1500 + 512 + 512 + 380 cycles), which the other row
 // block only partly covers. 16K tokens of 64/8 heads: 3.46 ms = 1270 TFLOP/s in a row of
-// five (power-capped clock), tensor pipe 54% active at 4K. A product of 64 keys costs the
+// five (power-capped clock; 3.42 to 3.53 in several calls), tensor pipe 54% active at 4K. A product of 64 keys costs the
 // cycles of one of 128, so smaller steps with two score buffers were slower (4.4 ms).
 // Bound of the weights: the exponential unit (73% active at 4K).
 #include <math.h>
@@ -316,6 +316,7 @@ struct Place {
 constexpr int kCleaners = 2;              // warps
 constexpr int kSoftWarps = 16;            // eight per row block, then products, loads, cleaners
 constexpr int kAttnThreads = 32 * (kSoftWarps + 2 + kCleaners);
+constexpr int kSoftRegs = 104, kOtherRegs = 64;   // of a thread, of the 640 x 96 launched
 constexpr uint32_t kAttnTmemCols = 512;   // S_0, S_1 (128 columns each), O_0, O_1
 
 template <int D>
@@ -364,14 +365,66 @@ __device__ __forceinline__ bool pair_any(int id, bool pred) {
     return r != 0;
 }
 
-// 32 scores of a row from TMEM; on the diagonal's tile those past column `lim` are masked.
-__device__ __forceinline__ void load_scores(uint32_t at, bool diagonal, int lim, uint32_t (&s)[32]) {
-    tmem_ld32(at, s);
-    if (diagonal) {
+// A thread's half of a row's scores (64, at ts), 32 at a time. kDiagonal: of the tile that the
+// diagonal crosses, 32 x 32 of a warp's scores lie before the diagonal (side + g < 0), on it or
+// (> 0) behind it, all masked. (The other tiles' loops are free of the tests: with
+// them in the loops 16K tokens took 3% longer.)
+template <bool kDiagonal>
+__device__ __forceinline__ float row_maximum(uint32_t ts, int side) {
+    const int lane = threadIdx.x & 31;
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-            if (c > lim) s[c] = 0xff800000u;
+    for (int g = 0; g < 2; ++g) {
+        if (kDiagonal && side + g > 0) continue;
+        uint32_t s[32];
+        tmem_ld32(ts + 32 * g, s);
+        if (kDiagonal && side + g == 0) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+                if (c > lane) s[c] = 0xff800000u;
+        }
+#pragma unroll
+        for (int c = 0; c < 32; c += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(s[c + i])), __uint_as_float(s[c + 4 + i]));
     }
+    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+
+// Their weights 2^(s sl - ms), bf16, to TMEM at tp (after `ready`), and their fp32 sum.
+template <bool kDiagonal, typename Ready>
+__device__ __forceinline__ float put_weights(uint32_t ts, uint32_t tp, int side, float sl, float ms, Ready ready) {
+    const int lane = threadIdx.x & 31;
+    const float2 sl2 = make_float2(sl, sl), ms2 = make_float2(-ms, -ms);
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        uint32_t w[16];
+        if (kDiagonal && side + g > 0) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) w[c] = 0u;
+        } else {
+            uint32_t s[32];
+            tmem_ld32(ts + 32 * g, s);
+            if (kDiagonal && side + g == 0) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    if (c > lane) s[c] = 0xff800000u;
+            }
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                float2 x = fma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sl2, ms2);
+                x = exp2_pair(x, c);
+                w[c] = bf16x2(x.x, x.y);
+                sum[c & 1] = add2(sum[c & 1], x);
+            }
+        }
+        if (g == 0) ready();
+        tmem_st16_issue(tp + 16 * g, w);
+    }
+    tmem_wait_st();
+    return (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
 }
 
 template <int D>
@@ -427,6 +480,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         return __all_sync(0xffffffffu, wait_or_dead(dead, bar, parity));
     };
 
+    // The 640 threads' 96 registers, divided anew (the launch checks that there are as many).
+    if (warp < kSoftWarps)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp < kSoftWarps) {  // softmax of row block b: half a row per thread
         const int b = warp >> 3, half = (warp >> 2) & 1, row = threadIdx.x & 127;
         const int pair_id = 1 + 4 * b + (warp & 3);
@@ -451,25 +509,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 last = k.last(b);
             }
             float m = -INFINITY, ms = 0.f;
-            float2 l2 = make_float2(0.f, 0.f);
+            float l = 0.f;   // this thread's half of the sum
             for (int j = 0; j <= last; ++j, par_s ^= 1) {
                 ok = wait(b_s + 8 * b, par_s);
-                const bool diagonal = j == last;
+                const int side = 2 * half - (warp & 3);
                 float mt = -INFINITY;
                 if (ok) {
                     tc_fence_after();
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        uint32_t s[32];
-                        load_scores(ts + 32 * g, diagonal, row - 64 * half - 32 * g, s);
-#pragma unroll
-                        for (int c = 0; c < 32; c += 8)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(s[c + i])), __uint_as_float(s[c + 4 + i]));
-                    }
-                    mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    mt = j < last ? row_maximum<false>(ts, side) : row_maximum<true>(ts, side);
                     // (the other thread has read the last one: it did so before its weights,
                     // which S_b's product waited for)
                     xch[half * kBlk] = mt;
@@ -495,8 +542,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                             m = mt;
                             ms = m * sl;
                         }
-                        l2.x *= al;
-                        l2.y *= al;
+                        l *= al;
 #pragma unroll 1
                         for (int c = 0; c < D / 2; c += 16) {
                             uint32_t o[16];
@@ -507,38 +553,25 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                         }
                     }
                 }
-                // the weights 2^(s sl - ms), bf16, over the first half of this thread's scores
-                const float2 sl2 = make_float2(sl, sl), ms2 = make_float2(-ms, -ms);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    uint32_t s[32], w[16];
-                    load_scores(ts + 32 * g, diagonal, row - 64 * half - 32 * g, s);
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        float2 x = fma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sl2, ms2);
-                        x = exp2_pair(x, c);
-                        w[c] = bf16x2(x.x, x.y);
-                        sum[c & 1] = add2(sum[c & 1], x);
-                    }
-                    if (C::kOwnP && g == 0) {  // the last P is no longer read (at the first: parity of no use)
+                auto ready = [&] {
+                    if (C::kOwnP) {  // the last P is no longer read (at the first: parity of no use)
                         wait(b_pv + 8 * b, par_s ^ 1);
                         tc_fence_after();
                     }
-                    tmem_st16_issue(tp + 16 * g, w);
-                }
-                tmem_wait_st();
-                l2 = add2(l2, add2(sum[0], sum[1]));
+                };
+                l += j < last ? put_weights<false>(ts, tp, side, sl, ms, ready)
+                              : put_weights<true>(ts, tp, side, sl, ms, ready);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_p + 8 * b);
             }
             if (ok) ok = wait(b_o + 8 * b, par_o) && wait(b_note + 8 * b, par_o);
             par_o ^= 1;
-            if (ok) xch[half * kBlk] = l2.x + l2.y;
+            if (ok) xch[half * kBlk] = l;
             if (pair_any(pair_id, !ok)) break;
             tc_fence_after();
-            const float l = xch[0] + xch[kBlk], inv = 1.f / l;
+            l = xch[0] + xch[kBlk];
+            const float inv = 1.f / l;
             const Item it = peek_item(ib, n);
             const Blocks k(it, group);
             const int qi = last * kBlk + row;
@@ -935,11 +968,13 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
                         if (!(ok = wait(b_s + 16 * w + 8 * buf.st, buf.par))) break;
                         tc_fence_after();
                         const int q0 = qs.q0(qt);
-                        const bool whole = q0 + 1 >= qs.key0 + (w + 1) * kBlk && q0 + kBlk <= qs.len;
                         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
+                            // of these 32 queries' columns those from the key on, within the prompt, count
                             const int col0 = 64 * half + 32 * g;
+                            const int first = qs.key0 + w * kBlk + 32 * (warp & 3) - q0 - col0;   // of the warp's first key
+                            const int end = qs.len - q0 - col0;
                             const float* lq = lse + at.st * kBlk + col0;
                             uint32_t s[32];
                             tmem_ld32(ts + kBlk * buf.st + 32 * g, s);
@@ -948,7 +983,8 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
                                 __syncwarp();
                                 if (lane == 0) mbar_arrive(b_sfree + 16 * w + 8 * buf.st);
                             }
-                            if (whole) {
+                            if (first > 31 || end <= 0) continue;   // none (of any of the warp's keys)
+                            if (first + 31 <= 0 && end >= 32) {     // all
 #pragma unroll
                                 for (int c = 0; c < 32; c += 4) {
                                     const float4 e = *reinterpret_cast<const float4*>(lq + c);
@@ -959,12 +995,12 @@ prefill_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_co
                                     acc[0] = add2(acc[0], exp2_pair(x, c / 2));
                                     acc[1] = add2(acc[1], exp2_pair(y, c / 2 + 1));
                                 }
-                            } else {  // the diagonal, or the prompt's end: some columns do not count
-                                const int lo = key - q0 - col0, hi = qs.len - q0 - col0;
+                            } else {  // the diagonal, or the prompt's end
+                                const int lo = first + lane;
 #pragma unroll
                                 for (int c = 0; c < 32; ++c) {
                                     const float x = ex2(fmaf(__uint_as_float(s[c]), sl, lq[c]));
-                                    if (c >= lo && c < hi) acc[c & 1].x += x;
+                                    if (c >= lo && c < end) acc[c & 1].x += x;
                                 }
                             }
                         }
@@ -1112,6 +1148,12 @@ cudaError_t launch_prefill_t(const PrefillParams& p, const CUtensorMap& qmap, co
     cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          C::kSmem);
     if (e != cudaSuccess) return e;
+    // what setmaxnreg hands out must have been launched, or its warps would wait for ever
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, prefill_kernel<D>);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs * kAttnThreads < 32 * (kSoftWarps * kSoftRegs + (kAttnThreads / 32 - kSoftWarps) * kOtherRegs))
+        return cudaErrorLaunchOutOfResources;
     const int64_t group = p.num_heads / p.num_kv_heads;
     // at least one more than there are pairs: its CTAs look every prompt over
     const int64_t pairs = ((int64_t)(p.total_tokens / kBlk + p.num_seqs) * group + p.num_seqs) / 2 + 1;
