@@ -205,8 +205,8 @@ def _dtype_code(t) -> int:
 def _on_current_device(t, name: str):
     """The library launches on the current device and stream: a tensor of another
     GPU would hand its kernels a pointer they cannot use."""
-    cur = _torch()._C._cuda_getDevice()
-    if t.get_device() != cur:
+    cur = _torch().cuda.current_device()
+    if t.device.index != cur:
         raise ValueError(f"{name} is on {t.device}, but the current CUDA device is cuda:{cur}; "
                          "call under torch.cuda.device(...) of the tensors' device")
 

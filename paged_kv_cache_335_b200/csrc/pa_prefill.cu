@@ -45,9 +45,10 @@
 // key tile and row block at head_dim 128), the exponential unit (16 per cycle and SM:
 // 1024 cycles per 128 x 128 weights) and, in between, the chain S -> softmax -> P V ->
 // next S of a row block (about 1500 + 512 + 512 + 380 cycles), which the other row
-// block only partly covers. 16K tokens of 64/8 heads: 3.46 ms = 1270 TFLOP/s in a row of
-// five (power-capped clock; 3.42 to 3.53 in several calls), tensor pipe 54% active at 4K. A product of 64 keys costs the
-// cycles of one of 128, so smaller steps with two score buffers were slower (4.4 ms).
+// block only partly covers. 16K tokens of 64/8 heads: 3.42 to 3.53 ms = 1250 to 1286
+// TFLOP/s in rows of five (power-capped clock), tensor pipe 54% active at 4K. A product of
+// 64 keys costs the cycles of one of 128, so smaller steps with two score buffers were
+// slower (4.4 ms).
 // Bound of the weights: the exponential unit (73% active at 4K).
 #include <math.h>
 
