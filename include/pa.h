@@ -568,8 +568,10 @@ int pa_rope_append_quant(void* q_out, const void* q, const void* k, const void* 
  *   cu_seqlens    device, int32 [num_seqs + 1], non-decreasing, in [0, total_tokens].
  *                 A prompt may be empty. Rows of no prompt (before the first, behind
  *                 the last) are neither read as keys nor written.
- *   max_seq_len   host bound on a prompt's length. A prompt with bad bounds or a
- *                 longer one is skipped and recorded as PA_ERR_BAD_INDEX.
+ *   max_seq_len   host bound on a prompt's length. A prompt with bad bounds (a row outside
+ *                 [0, total_tokens), an end before its start, a first row before the end
+ *                 of an earlier prompt) or a longer one is skipped and recorded as
+ *                 PA_ERR_BAD_INDEX.
  * A query's result depends on its own prompt's rows 0 .. i alone, bit for bit, whatever
  * the other rows hold (infinities and NaN too) and whatever else is in the call.
  * bf16: products on the tensor cores with fp32 sums; the softmax weights are rounded to

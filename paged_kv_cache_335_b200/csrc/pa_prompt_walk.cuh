@@ -20,30 +20,50 @@ struct PromptTile {
 // of the 32 those with the most work come first: rank r of a prompt's `count` tiles is
 // tile r when `reversed` (a query tile attends to the tiles before it), else tile
 // count - 1 - r (a key tile is attended to by those behind it), and the ranks descend. A
-// prompt with bad bounds (outside [0, total_tokens], negative length, or longer than
-// max_seq_len) has no tile; `bad` reports that the lane met one. Indices that ascend read
-// each prompt once.
+// prompt with bad bounds (outside [0, total_tokens], negative length, longer than max_seq_len,
+// or with a first row before the end of an earlier prompt) has no tile; `bad` reports that the
+// lane met one. So the prompts that have tiles are disjoint, and all their tiles of B tokens are
+// at most total_tokens / B + num_seqs. Indices that ascend read each prompt once.
 struct PromptWalk {
     int base = 0;      // prompts of the lanes: base ..
     int seen = 0;      // tiles before them
     int start = 0, len = 0, count = 0;   // the lane's prompt
     int total = 0;     // tiles of the 32
+    int reach = 0, next_reach = 0;       // the furthest end of the prompts before the 32, and with them
     int rank = 0, above = 0, upto = 0;   // the last rank, tiles of higher ranks, and with this one's
     bool loaded = false, bad = false;
 
     template <typename Tiles>
     __device__ __forceinline__ void load(const PrefillParams& p, Tiles tiles) {
-        const int s = base + (threadIdx.x & 31);
+        const int lane = threadIdx.x & 31, s = base + lane;
         start = len = 0;
+        int end = 0;
+        bool descends = false;
         if (s < p.num_seqs) {
             start = __ldg(p.cu_seqlens + s);
-            const int b = __ldg(p.cu_seqlens + s + 1);
-            len = b - start;
-            if (start < 0 || b < start || b > p.total_tokens || len > p.max_seq_len) {
+            end = __ldg(p.cu_seqlens + s + 1);
+            len = end - start;
+            descends = end < start;
+            if (start < 0 || end < start || end > p.total_tokens || len > p.max_seq_len) {
+                bad = true;
+                len = end = 0;
+            }
+        }
+        // Bounds that never descend hold no overlap.
+        if (__any_sync(0xffffffffu, descends || (len > 0 && start < reach))) {
+            int far = end;   // the furthest end up to each prompt, then before it
+#pragma unroll 1
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, far, off);
+                if (lane >= off) far = max(far, y);
+            }
+            far = __shfl_up_sync(0xffffffffu, far, 1);
+            if (len > 0 && start < (lane > 0 ? max(far, reach) : reach)) {
                 bad = true;
                 len = 0;
             }
         }
+        next_reach = max(reach, __reduce_max_sync(0xffffffffu, end));
         count = tiles(len);
         total = __reduce_add_sync(0xffffffffu, count);
         rank = above = upto = 0;   // (the rank of the 32 before means nothing here: the next search starts anew)
@@ -61,7 +81,7 @@ struct PromptWalk {
         t.seq = -1;
         t.start = t.len = t.tile = 0;
         if (u < seen) {  // behind an index that came before: from the start again
-            base = seen = 0;
+            base = seen = reach = 0;
             loaded = false;
         }
         if (!loaded) load(p, tiles);
@@ -69,6 +89,7 @@ struct PromptWalk {
             if (base + 32 >= p.num_seqs) return t;
             base += 32;
             seen += total;
+            reach = next_reach;
             load(p, tiles);
         }
         // the rank: from_rank(rank) > v >= from_rank(rank + 1); mostly the last one still

@@ -89,6 +89,7 @@ unsigned __ballot_sync(unsigned, bool v) {
     for (int l = 0; l < kLanes; ++l) b |= (a[l] ? 1u : 0u) << l;
     return b;
 }
+bool __any_sync(unsigned m, bool v) { return __ballot_sync(m, v) != 0; }
 int __shfl_sync(unsigned, int v, int src) { return meet(v)[src & 31]; }
 int __shfl_up_sync(unsigned, int v, int d) {
     const int l = g_warp->cur;

@@ -55,3 +55,24 @@ def test_weights_of_many_prompts(lens, h, hkv, d, dtype, last):
         tol = P.EPS32 * (mag + ref * ((h // hkv) * n + 16)) + 1e-37
         err = (w[s, :, :n].double() - ref).abs()
         assert bool((err <= tol).all()), f"prompt {s}: {float((err / tol).max()):.2f} of the bound"
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_overlapping_prompts_are_skipped(dtype):
+    """The third prompt's rows are the first one's: the first is whole, the third reported."""
+    h, hkv, d = 4, 2, 64
+    q, k, v, cu, _ = _inputs([700], h, hkv, d, dtype, seed=3)
+    cut = torch.tensor([0, 700, 0, 700], dtype=torch.int32, device=DEV)
+    out = torch.full(q.shape, 7.0, device=DEV, dtype=dtype)
+    lse = torch.full((h, 700), 7.0, device=DEV)
+    w = torch.full((3, hkv, 700), 7.0, device=DEV)
+    for call in (lambda: pa.pa_prefill(out, q, k, v, cut, 0.125, max_seq_len=700, lse=lse),
+                 lambda: pa.pa_prefill_weights(w, q, k, lse, cut, 0.125, max_seq_len=700)):
+        call()
+        with pytest.raises(pa.PAError) as e:
+            pa.pa_sync_check()
+        assert e.value.code == pa.PA_ERR_BAD_INDEX
+    _check([700], h, hkv, d, dtype, 0.125, q, k, v, cu, out, lse)
+    total = w.sum(-1)
+    assert torch.allclose(total[0], torch.full_like(total[0], 700.0 * h / hkv), rtol=1e-3)
+    assert not w[1:].any()

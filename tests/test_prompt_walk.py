@@ -96,3 +96,20 @@ def test_bad_prompts_have_no_tile(host):
         assert bad
         want = sorted((s, t) for s, n in good.items() for t in range(-(-n // 64)))
         assert sorted((t[0], t[3]) for t in got if t[0] >= 0) == want
+
+
+@pytest.mark.parametrize("cu,good", [
+    ([0, 300, 0, 300], {0}),                             # the third prompt holds the first one's rows
+    ([0, 200, 190, 310], {0}),
+    ([0, 100, 500, 90, 95, 120, 130], {0, 5}),           # 100..500 lies outside; 90..95 and 95..120 come too early
+    ([0, 10] + [10] * 30 + [310, 0, 200, 200, 310], {0, 31}),   # across the 32
+    ([200, 310, 0, 100], {0}),
+])
+def test_prompts_that_overlap_an_earlier_one_have_no_tile(host, cu, good):
+    """The grids are sized for disjoint prompts: total tokens / tile + prompts."""
+    for block in (64, 128):
+        got, bad = _walk(host, cu, 310, 310, block, 1, 1, True, range(100))
+        assert bad
+        want = sorted((s, t) for s in good for t in range(-(-(cu[s + 1] - cu[s]) // block)))
+        assert sorted((t[0], t[3]) for t in got if t[0] >= 0) == want
+        assert len(want) <= 310 // block + len(cu) - 1
