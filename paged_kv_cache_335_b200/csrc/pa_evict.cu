@@ -559,12 +559,15 @@ add_weights_kernel(const AddWeightsParams p) {
 }  // namespace
 
 template <int kThreads>
-static size_t evict_smem_bytes(int max_context_len, bool keys) {
+static constexpr size_t evict_smem_bytes(int max_context_len, bool keys) {
     const size_t words = ((size_t)max_context_len + 127) / 128 * 4;
     return 4 * (2 * words + Select<kThreads>::kListCap + kMaxWarps + 4 + (keys ? 32 * words : 0));
 }
 
-int evict_max_context() { return (int)((227 * 1024 - evict_smem_bytes<1024>(0, false)) / 32 * 128); }
+constexpr size_t kMaxSmem = 227 * 1024;
+constexpr int kShortContext = 4096;   // contexts up to this take the 256-thread form
+
+int evict_max_context() { return (int)((kMaxSmem - evict_smem_bytes<1024>(0, false)) / 32 * 128); }
 
 // A kernel that starts while the one before it ends (it waits for it itself).
 template <typename K>
@@ -585,9 +588,12 @@ static cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t sme
 
 template <int kThreads, bool kShared, bool kMove>
 static cudaError_t launch_select(const EvictParams& p, cudaStream_t stream) {
+    // The limit is the kernel's, for every host thread at once: the same in every call, whatever
+    // this one takes.
     const size_t smem = evict_smem_bytes<kThreads>(p.max_context_len, kShared);
+    const size_t limit = kThreads == 256 ? evict_smem_bytes<kThreads>(kShortContext, kShared) : kMaxSmem;
     cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<kThreads, kShared, kMove>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit);
     if (e != cudaSuccess) return e;
     evict_select_kernel<kThreads, kShared, kMove>
         <<<dim3((unsigned)p.num_kv_heads, (unsigned)p.num_seqs), kThreads, smem, stream>>>(p);
@@ -599,10 +605,10 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
     // A row of a short context is bound by its barriers: fewer threads, more rows per SM. Where such
     // rows fill the SMs, each also moves its own keys and values: 16 x 40 rows of 2064
     // tokens take 19.7 us on the device, with the two further launches 20.5 and 4 us more of host time.
-    if (p.max_context_len <= 4096 && (int64_t)rows.x * rows.y >= 148)
+    if (p.max_context_len <= kShortContext && (int64_t)rows.x * rows.y >= 148)
         return launch_select<256, true, true>(p, stream);
-    cudaError_t e = p.max_context_len <= 4096 ? launch_select<256, true, false>(p, stream)
-                    : evict_smem_bytes<1024>(p.max_context_len, true) <= 227 * 1024
+    cudaError_t e = p.max_context_len <= kShortContext ? launch_select<256, true, false>(p, stream)
+                    : evict_smem_bytes<1024>(p.max_context_len, true) <= kMaxSmem
                         ? launch_select<1024, true, false>(p, stream)
                         : launch_select<1024, false, false>(p, stream);
     if (e != cudaSuccess) return e;

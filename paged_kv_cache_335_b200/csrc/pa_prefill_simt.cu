@@ -304,9 +304,11 @@ cudaError_t launch_prefill_t(const PrefillParams& p, cudaStream_t stream) {
     // 156). With no more than two per SM in all, the longest tile's time is the kernel's, and it
     // is shorter alone, the others queueing for the SMs that finish (280 CTAs: 77 us
     // against 92): more shared memory than half an SM's keeps a second one away.
-    const size_t smem = ctas <= 2 * 148 ? std::max(smem_prefill<D>(), (size_t)120 * 1024) : smem_prefill<D>();
+    constexpr size_t alone = std::max(smem_prefill<D>(), (size_t)120 * 1024);
+    const size_t smem = ctas <= 2 * 148 ? alone : smem_prefill<D>();
+    // (the limit is the kernel's, for every host thread at once: the same in every call)
     cudaError_t e = cudaFuncSetAttribute(prefill_simt_kernel<D>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)alone);
     if (e != cudaSuccess) return e;
     prefill_simt_kernel<D><<<(unsigned)ctas, kThreads, smem, stream>>>(p);
     return cudaGetLastError();
