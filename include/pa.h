@@ -533,8 +533,10 @@ typedef struct pa_rope_desc {
  *   q, k, v       device, the cache's type, token strides as above.
  *   positions     device, int32 [num_axes][num_tokens]; any value, negative too.
  *   slot_mapping  device, int64 [num_tokens].
- * The angle is reduced exactly in 64-bit fixed point, so positions of any size keep
- * the full fp32 accuracy of the sine and cosine. num_heads >= 0: with 0 only k and v
+ * The angle is held as a fraction of a turn in 64-bit fixed point, off by at most
+ * |position| (1 + |inv_freq|) 2^-65 turns whatever the position's size, and rounded once to
+ * fp32 half-turns (a small angle to 24 bits of its own) before its sine and cosine are
+ * formed in fp32. num_heads >= 0: with 0 only k and v
  * are appended (q and q_out may then be NULL).
  *
  * pa_rope_append_quant — the same into a quantised cache: q, k, v and q_out bf16, each

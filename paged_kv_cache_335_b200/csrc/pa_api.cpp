@@ -4,7 +4,6 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
-#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -543,10 +542,12 @@ static int rope_impl(void* q_out, const void* q, const void* k, const void* v, i
             return fail(PA_ERR_INVALID_ARG, "inv_freq[%d] is not finite", i);
         if (rope->axis[i] >= rope->num_axes)
             return fail(PA_ERR_INVALID_ARG, "axis[%d] = %d, num_axes %d", i, rope->axis[i], rope->num_axes);
-        // turns per position modulo 1, in units of 2^-64 (64-bit significand)
-        long double t = (long double)rope->inv_freq[i] * 0.15915494309189533576888376337251L;
-        if (t < 0 || t >= 1) t -= std::floor(t);
-        p.turns[i] = (uint64_t)std::min(18446744073709551615.0L, t * 0x1p64L);
+        // turns per position modulo 1, rounded to units of 2^-64. The product has a 64-bit
+        // significand: its error, and that of 1 / 2 pi in it, are below |inv_freq| 2^-65 turns.
+        long double t = std::fabs((long double)rope->inv_freq[i]) * 0.15915494309189533576888376337251L;
+        t = std::rint((t - std::floor(t)) * 0x1p64L);
+        const uint64_t u = t >= 0x1p64L ? 0 : (uint64_t)t;
+        p.turns[i] = rope->inv_freq[i] < 0 ? 0 - u : u;
         p.axis[i] = rope->axis[i];
     }
     if (num_heads < 0 || num_heads > 65535)

@@ -11,10 +11,11 @@
 //
 // The angle is formed as a fraction of a turn in 64-bit fixed point: turns[i] =
 // inv_freq[i] / (2 pi) modulo 1, in units of 2^-64, times the integer position,
-// modulo 2^64. That reduction loses nothing to the position's size (the error
-// is at most |position| * 2^-65 turns), where a 32-bit float product of a
-// position near 10^5 would be off by 10^-2 radians. sincospif takes the top 32
-// bits.
+// modulo 2^64. Only the rounding of turns[i] grows with the position (the angle is off by
+// at most |position| (1 + |inv_freq|) 2^-65 turns), where a 32-bit float product of a
+// position near 10^5 would be off by 10^-2 radians. All 64 bits are then rounded once to
+// fp32 half-turns in [-1, 1] for sincospif, so that a small angle, whose leading bits are
+// zeros or ones, keeps 24 bits of its own.
 //
 // Bound by HBM for prompts and by launch latency for a decode step, so: every
 // thread moves units of 16 elements (32 bytes of bf16), kept as loaded until the table of
@@ -153,7 +154,7 @@ rope_append_kernel(const __grid_constant__ RopeParams p) {
         const int32_t pos = __ldg(p.positions + (int64_t)p.axis[f] * p.num_tokens + token0 + t);
         const uint64_t turn = (uint64_t)(int64_t)pos * p.turns[f];
         float s, c;
-        sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
+        sincospif((float)(int64_t)turn * 0x1p-63f, &s, &c);
         table[t][f] = make_float2(c * p.mscale, s * p.mscale);
     }
     __syncthreads();
