@@ -16,6 +16,7 @@ Cache layout: ``k_cache``/``v_cache`` are ``[num_blocks][num_kv_heads]
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -240,6 +241,47 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _on(stream):
+    """Context in which torch's own part of a call runs on the call's stream: a maximum reads what
+    that stream has written, and a temporary workspace goes back to that stream's memory."""
+    if stream is None:
+        return contextlib.nullcontext()
+    cuda = _torch().cuda
+    if not isinstance(stream, cuda.Stream):
+        handle = _stream(stream)
+        stream = cuda.ExternalStream(0 if handle == 1 else handle)  # 1: the legacy default stream
+    return cuda.stream(stream)
+
+
+def _longest(lens, stream) -> int:
+    """The largest of the device's ``lens`` (a sync of the call's stream)."""
+    if not lens.numel():
+        return 0
+    with _on(stream):
+        return int(lens.max().item())
+
+
+def _longest_between(bounds, stream) -> int:
+    """The largest distance between consecutive entries of the device's ``bounds``."""
+    if bounds.numel() < 2:
+        return 0
+    with _on(stream):
+        return int((bounds[1:] - bounds[:-1]).max().item())
+
+
+def _workspace(need, workspace, device, stream):
+    """The caller's workspace, or one allocated for the call, with its pointer and bytes. The
+    caller of this holds the tensor until its launch is enqueued: from then on only what the same
+    stream does later can be given its memory."""
+    if not need:
+        return None, 0, 0
+    if workspace is None:
+        torch = _torch()
+        with _on(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+
+
 def cache_desc(k_cache) -> pa_cache_desc:
     """Descriptor of a ``[num_blocks][num_kv_heads][block_size][head_dim]`` pool tensor."""
     if k_cache.dim() != 4:
@@ -315,13 +357,9 @@ def pa_decode_quant(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, co
     if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
         raise TypeError("q and out must be bfloat16")
     if max_context_len is None:
-        max_context_len = int(context_lens.max().item()) if s else 0
+        max_context_len = _longest(context_lens, stream)
     need = pa_decode_workspace_size(s, h, max_context_len, k_cache, partition_size)
-    ws_ptr, ws_bytes = ctypes.c_void_p(0), 0
-    if need:
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        ws_ptr, ws_bytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    ws, ws_ptr, ws_bytes = _workspace(need, workspace, q.device, stream)
     _check(load_library().pa_decode_quant(
         _dev(out, "out"), _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
         _dev(k_scale, "k_scale", torch.float32), _dev(v_scale, "v_scale", torch.float32),
@@ -329,15 +367,6 @@ def pa_decode_quant(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, co
         _dev(context_lens, "context_lens", torch.int32), int(max_context_len), s, h,
         float(scale), ctypes.byref(desc), int(partition_size), ws_ptr, ws_bytes,
         _stream(stream)))
-
-
-def _quant_ws(need, workspace, device):
-    torch = _torch()
-    if not need:
-        return ctypes.c_void_p(0), 0
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
 
 
 def pa_decode_grouped_quant(out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
@@ -355,10 +384,10 @@ def pa_decode_grouped_quant(out, q, k_cache, v_cache, k_scale, v_scale, block_ta
     if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
         raise TypeError("q and out must be bfloat16")
     if max_context_len is None:
-        max_context_len = int(context_lens.max().item()) if s else 0
+        max_context_len = _longest(context_lens, stream)
     need = pa_decode_grouped_workspace_size(s, h, max_context_len, k_cache, int(group_size),
                                             partition_size)
-    ws_ptr, ws_bytes = _quant_ws(need, workspace, q.device)
+    ws, ws_ptr, ws_bytes = _workspace(need, workspace, q.device, stream)
     _check(load_library().pa_decode_grouped_quant(
         _dev(out, "out"), _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
         _dev(k_scale, "k_scale", torch.float32), _dev(v_scale, "v_scale", torch.float32),
@@ -385,12 +414,12 @@ def pa_decode_multi_quant(out, q, k_cache, v_cache, k_scale, v_scale, block_tabl
     if block_tables.dim() != 2 or block_tables.shape[0] != s or query_start.shape != (s + 1,):
         raise ValueError("block_tables [S][stride], context_lens [S], query_start [S + 1]")
     if max_context_len is None:
-        max_context_len = int(context_lens.max().item()) if s else 0
+        max_context_len = _longest(context_lens, stream)
     if max_query_len is None:
-        max_query_len = max(1, int((query_start[1:] - query_start[:-1]).max().item())) if s else 1
+        max_query_len = max(1, _longest_between(query_start, stream))
     need = pa_decode_multi_workspace_size(s, t, max_query_len, h, max_context_len, k_cache,
                                           partition_size)
-    ws_ptr, ws_bytes = _quant_ws(need, workspace, q.device)
+    ws, ws_ptr, ws_bytes = _workspace(need, workspace, q.device, stream)
     _check(load_library().pa_decode_multi_quant(
         _dev(out, "out"), _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
         _dev(k_scale, "k_scale", torch.float32), _dev(v_scale, "v_scale", torch.float32),
@@ -481,14 +510,10 @@ def _decode_call(entry, extra, out, q, k_cache, v_cache, block_tables, context_l
     if block_tables.dim() != 2 or block_tables.shape[0] != s or context_lens.shape != (s,):
         raise ValueError("block_tables must be [num_seqs][stride], context_lens [num_seqs]")
     if max_context_len is None:
-        max_context_len = int(context_lens.max().item()) if s else 0
+        max_context_len = _longest(context_lens, stream)
     need = pa_decode_grouped_workspace_size(s, h, max_context_len, k_cache, group_size,
                                             partition_size)
-    ws_ptr, ws_bytes = ctypes.c_void_p(0), 0
-    if need:
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        ws_ptr, ws_bytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    ws, ws_ptr, ws_bytes = _workspace(need, workspace, q.device, stream)
     _check(entry(
         _dev(out, "out"), _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
         _dev(block_tables, "block_tables", torch.int32), int(block_tables.shape[1]),
@@ -571,16 +596,12 @@ def pa_decode_multi(out, q, k_cache, v_cache, block_tables, context_lens, query_
     if block_tables.dim() != 2 or block_tables.shape[0] != s or query_start.shape != (s + 1,):
         raise ValueError("block_tables [S][stride], context_lens [S], query_start [S + 1]")
     if max_context_len is None:
-        max_context_len = int(context_lens.max().item()) if s else 0
+        max_context_len = _longest(context_lens, stream)
     if max_query_len is None:
-        max_query_len = max(1, int((query_start[1:] - query_start[:-1]).max().item())) if s else 1
+        max_query_len = max(1, _longest_between(query_start, stream))
     need = pa_decode_multi_workspace_size(s, t, max_query_len, h, max_context_len, k_cache,
                                           partition_size)
-    ws_ptr, ws_bytes = ctypes.c_void_p(0), 0
-    if need:
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        ws_ptr, ws_bytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    ws, ws_ptr, ws_bytes = _workspace(need, workspace, q.device, stream)
     _check(load_library().pa_decode_multi(
         _dev(out, "out"), _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
         _dev(block_tables, "block_tables", torch.int32), int(block_tables.shape[1]),
@@ -606,7 +627,7 @@ def pa_decode_noalloc(out, q, k_cache, v_cache, block_tables, context_lens, scal
     if block_tables.dim() != 2 or block_tables.shape[0] != s or context_lens.shape != (s,):
         raise ValueError("block_tables must be [num_seqs][stride], context_lens [num_seqs]")
     if max_context_len is None:
-        max_context_len = int(context_lens.max().item()) if s else 0
+        max_context_len = _longest(context_lens, stream)
     _check(load_library().pa_decode_noalloc(
         _dev(out, "out"), _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
         _dev(block_tables, "block_tables", torch.int32), int(block_tables.shape[1]),
@@ -702,7 +723,7 @@ def pa_rope_append_quant(q_out, q, k, v, positions, slot_mapping, k_cache, v_cac
                slot_mapping, k_cache, v_cache, rope, _torch().bfloat16, stream)
 
 
-def _prompt_shapes(q, k, cu_seqlens, max_seq_len):
+def _prompt_shapes(q, k, cu_seqlens, max_seq_len, stream):
     if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
         raise ValueError("q must be [total_tokens][num_heads][head_dim], k and v "
                          "[total_tokens][num_kv_heads][head_dim]")
@@ -710,7 +731,7 @@ def _prompt_shapes(q, k, cu_seqlens, max_seq_len):
         raise ValueError("cu_seqlens must be [num_seqs + 1]")
     s = int(cu_seqlens.shape[0]) - 1
     if max_seq_len is None:
-        max_seq_len = int((cu_seqlens[1:] - cu_seqlens[:-1]).max().item()) if s else 0
+        max_seq_len = _longest_between(cu_seqlens, stream)
     return s, int(max_seq_len)
 
 
@@ -721,7 +742,7 @@ def pa_prefill(out, q, k, v, cu_seqlens, scale: float, max_seq_len: int | None =
     log-sum-exp. ``max_seq_len`` is a host bound on the prompts' lengths (computed with a
     device sync if omitted)."""
     torch = _torch()
-    s, max_seq_len = _prompt_shapes(q, k, cu_seqlens, max_seq_len)
+    s, max_seq_len = _prompt_shapes(q, k, cu_seqlens, max_seq_len, stream)
     if out.shape != q.shape or v.shape != k.shape:
         raise ValueError("out must have q's shape and v k's")
     t, h, d = (int(x) for x in q.shape)
@@ -743,7 +764,7 @@ def pa_prefill_weights(weights, q, k, lse, cu_seqlens, scale: float,
     prompt token t received, summed over the heads of kv head kh and the prompt's queries (its
     last ``last_queries`` ones if > 0). ``lse`` as pa_prefill returned it."""
     torch = _torch()
-    s, max_seq_len = _prompt_shapes(q, k, cu_seqlens, max_seq_len)
+    s, max_seq_len = _prompt_shapes(q, k, cu_seqlens, max_seq_len, stream)
     t, h, d = (int(x) for x in q.shape)
     if weights.dim() != 3 or tuple(weights.shape[:2]) != (s, int(k.shape[1])):
         raise ValueError("weights must be [num_seqs][num_kv_heads][weights_stride]")
@@ -790,9 +811,9 @@ def _decode_weights_call(entry, scales, out, weights, q, k_cache, v_cache, block
         if tuple(x.shape) != (desc.num_kv_heads,):
             raise ValueError("k_scale and v_scale must be [num_kv_heads]")
     if max_context_len is None:
-        max_context_len = int(context_lens.max().item()) if s else 0
+        max_context_len = _longest(context_lens, stream)
     need = pa_decode_weights_workspace_size(s, h, max_context_len, k_cache, partition_size)
-    ws_ptr, ws_bytes = _quant_ws(need, workspace, q.device)
+    ws, ws_ptr, ws_bytes = _workspace(need, workspace, q.device, stream)
     _check(entry(
         _dev(out, "out"), _dev(weights, "weights", torch.float32), int(weights.shape[2]),
         _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
@@ -844,7 +865,7 @@ def pa_evict(k_cache, v_cache, block_tables, context_lens, weights, weights_out,
     if tuple(kept.shape) != (s, desc.num_kv_heads, int(budget)):
         raise ValueError("kept must be [num_seqs][num_kv_heads][budget]")
     if max_context_len is None:
-        max_context_len = int(context_lens.max().item()) if s else 0
+        max_context_len = _longest(context_lens, stream)
     _check(load_library().pa_evict(
         _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
         _dev(block_tables, "block_tables", torch.int32), int(block_tables.shape[1]),
