@@ -210,7 +210,8 @@ __device__ __forceinline__ int block_scan_exclusive(int v, int* sm, int& total) 
 }
 
 // f(word, key, token exists) for each word of the warp's run w0 .. w1, in order; keys of the
-// first `cand` tokens, from shared memory or made of the weights.
+// first `cand` tokens, from shared memory or made of the weights. (The weights are read by
+// plain loads: the read-only path is not for what this kernel may overwrite in place.)
 template <bool kShared, typename F>
 __device__ __forceinline__ void each_word(const float* w, const uint32_t* keys, int w0, int w1, int cand, F f) {
     const int lane = threadIdx.x & 31;
@@ -220,7 +221,7 @@ __device__ __forceinline__ void each_word(const float* w, const uint32_t* keys, 
         for (int e = 0; e < kBatch; ++e) {
             const int t = 32 * (i + e) + lane;
             k[e] = 0u;
-            if (i + e < w1 && t < cand) k[e] = kShared ? keys[t] : weight_key(__ldg(w + t));
+            if (i + e < w1 && t < cand) k[e] = kShared ? keys[t] : weight_key(w[t]);
         }
 #pragma unroll
         for (int e = 0; e < kBatch; ++e)
@@ -247,14 +248,14 @@ __device__ __forceinline__ int select_row(const float* w, int cand, int edge, ui
             float4 x[kBatch];
 #pragma unroll
             for (int e = 0; e < kBatch; ++e)
-                if (i0 + e * kThreads < quads) x[e] = __ldg(reinterpret_cast<const float4*>(w) + i0 + e * kThreads);
+                if (i0 + e * kThreads < quads) x[e] = reinterpret_cast<const float4*>(w)[i0 + e * kThreads];
 #pragma unroll
             for (int e = 0; e < kBatch; ++e)
                 if (i0 + e * kThreads < quads)
                     reinterpret_cast<uint4*>(keys)[i0 + e * kThreads] =
                         make_uint4(weight_key(x[e].x), weight_key(x[e].y), weight_key(x[e].z), weight_key(x[e].w));
         }
-        for (int t = 4 * quads + tid; t < cand; t += kThreads) keys[t] = weight_key(__ldg(w + t));
+        for (int t = 4 * quads + tid; t < cand; t += kThreads) keys[t] = weight_key(w[t]);
         __syncthreads();
     }
     // The edge-th largest key among the candidates, and how many of the tokens
