@@ -58,7 +58,8 @@ class BlockManager:
         # pop() takes from the end: reverse so that order[0] is handed out first.
         self._free = [i for i in reversed(ids) if i not in reserved]
         self.refcount = np.zeros(num_blocks, dtype=np.int64)
-        self.copies: list = []  # (src, dst) pairs recorded by copy-on-write
+        self._copies: dict = {}   # dst: src of the copies recorded since take_copies
+        self._sources: dict = {}  # how many of them read a block
 
     # -- pool ---------------------------------------------------------------
     @property
@@ -68,7 +69,10 @@ class BlockManager:
     def allocate(self) -> int:
         if not self._free:
             raise PoolExhausted(f"no free block left in a pool of {self.num_blocks}")
-        b = self._free.pop()
+        return self._take(len(self._free) - 1)
+
+    def _take(self, i: int) -> int:
+        b = self._free.pop(i)
         assert self.refcount[b] == 0
         self.refcount[b] = 1
         return b
@@ -78,7 +82,37 @@ class BlockManager:
             raise AssertionError(f"block {b} released with refcount {self.refcount[b]}")
         self.refcount[b] -= 1
         if self.refcount[b] == 0:
+            if b in self._copies:  # nobody needs its copy any more
+                src = self._copies.pop(b)
+                self._sources[src] -= 1
+                if self._sources[src] == 0:
+                    del self._sources[src]
             self._free.append(b)
+
+    # -- copies -------------------------------------------------------------
+    # The pairs of one pa_block_copy are copied in any order: a target occurs once and is no
+    # source. So a copy of a block that itself waits for its copy reads that one's source, and a
+    # freed block that a recorded copy still reads is not taken as a target before
+    # take_copies. (It may hold a new token: appends come after the copies.)
+    @property
+    def copies(self) -> list:
+        """(src, dst) pairs recorded since take_copies."""
+        return [(src, dst) for dst, src in self._copies.items()]
+
+    def _num_targets(self) -> int:
+        """Free blocks that a copy may go to now."""
+        return self.num_free - (sum(b in self._sources for b in self._free) if self._sources else 0)
+
+    def _private_copy(self, b: int) -> int:
+        """A block of the caller's own in place of its reference to ``b``; the copy is recorded."""
+        i = next((i for i in range(len(self._free) - 1, -1, -1) if self._free[i] not in self._sources), -1)
+        if i < 0:
+            raise PoolExhausted(f"no free block left for a copy in a pool of {self.num_blocks}")
+        nb, src = self._take(i), self._copies.get(b, b)
+        self._copies[nb] = src
+        self._sources[src] = self._sources.get(src, 0) + 1
+        self.refcount[b] -= 1
+        return nb
 
     # -- sequences ----------------------------------------------------------
     def new_sequence(self, length: int = 0) -> Sequence:
@@ -106,8 +140,8 @@ class BlockManager:
 
         If the position opens a new block, a block is allocated. If it falls in
         a block that other sequences still reference, the block is first
-        replaced by a private copy and the (src, dst) pair is recorded in
-        ``self.copies`` for ``pa_block_copy``.
+        replaced by a private copy and the (src, dst) pair is recorded for
+        ``take_copies``.
         """
         pos = seq.length
         j, off = divmod(pos, self.block_size)
@@ -116,25 +150,20 @@ class BlockManager:
         else:
             b = seq.table[j]
             if self.refcount[b] > 1:
-                nb = self.allocate()
-                self.copies.append((b, nb))
-                self.refcount[b] -= 1
-                seq.table[j] = nb
+                seq.table[j] = self._private_copy(b)
         seq.length = pos + 1
         return seq.table[j] * self.block_size + off
 
     def unshare(self, seq: Sequence) -> int:
         """Replace every block of ``seq`` that others still reference by a private copy, as
         rows about to move inside it require (``pa_evict``); the (src, dst) pairs are recorded
-        in ``self.copies``. Returns how many."""
+        for ``take_copies``. Returns how many."""
         shared = [j for j, b in enumerate(seq.table) if self.refcount[b] > 1]
-        if len(shared) > self.num_free:
-            raise PoolExhausted(f"{len(shared)} shared blocks to copy, {self.num_free} free")
+        targets = self._num_targets()
+        if len(shared) > targets:
+            raise PoolExhausted(f"{len(shared)} shared blocks to copy, {targets} free")
         for j in shared:
-            b, nb = seq.table[j], self.allocate()
-            self.copies.append((b, nb))
-            self.refcount[b] -= 1
-            seq.table[j] = nb
+            seq.table[j] = self._private_copy(seq.table[j])
         return len(shared)
 
     def truncate(self, seq: Sequence, length: int) -> None:
@@ -149,9 +178,10 @@ class BlockManager:
         seq.length = length
 
     def take_copies(self) -> np.ndarray:
-        """Copy pairs recorded since the last call, as int64 [P][2]."""
+        """Copy pairs recorded since the last call, as int64 [P][2], for ``pa_block_copy`` ahead of
+        whatever else is written to the pool."""
         pairs = np.asarray(self.copies, dtype=np.int64).reshape(-1, 2)
-        self.copies = []
+        self._copies, self._sources = {}, {}
         return pairs
 
     # -- views --------------------------------------------------------------
