@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -518,6 +519,21 @@ static int decode_impl(void* out, const void* q, const void* k_cache, const void
     return PA_OK;
 }
 
+// The status words of the calls around decode. Reading one takes 10 us, so pa_sync_check reads
+// those whose call was made (or captured: a replay tells the host nothing) since the process
+// began: all of them took it from 29 to 70 us.
+struct AroundDecode {
+    cudaError_t (*read)(unsigned*, bool);
+    bool beside_copies;
+    std::atomic<bool> called;
+};
+static AroundDecode g_around_decode[] = {{pa::read_status_rope, true, {false}},
+                                         {pa::read_status_evict, true, {false}},
+                                         {pa::read_status_prefill, false, {false}},
+                                         {pa::read_status_prefill_simt, false, {false}}};
+enum { kRope, kEvict, kPrefill, kPrefillSimt };
+static void mark_called(int word) { g_around_decode[word].called.store(true, std::memory_order_release); }
+
 // pa_rope_append / pa_rope_append_quant (k_scale, v_scale set).
 static int rope_impl(void* q_out, const void* q, const void* k, const void* v, int64_t q_stride,
                      int64_t k_stride, int64_t v_stride, const int32_t* positions,
@@ -602,6 +618,7 @@ static int rope_impl(void* q_out, const void* q, const void* k, const void* v, i
     p.adjacent = rope->pairs == PA_ROPE_ADJACENT;
     p.tokens_per_cta = 1;
     p.mscale = rope->mscale;
+    mark_called(kRope);
     cudaError_t ce = pa::launch_rope_append(p, cache->dtype, static_cast<cudaStream_t>(stream));
     return ce == cudaSuccess ? PA_OK : fail_cuda(ce, "pa_rope_append launch");
 }
@@ -967,6 +984,7 @@ int pa_prefill(void* out, const void* q, const void* k, const void* v, int64_t q
     p.lse = lse;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t ce;
+    mark_called(dtype == PA_F32 ? kPrefillSimt : kPrefill);
     if (dtype == PA_F32) {
         ce = pa::launch_prefill_simt(p, st);
     } else {
@@ -1012,6 +1030,7 @@ int pa_prefill_weights(float* weights, int64_t weights_stride, const void* q, co
     cudaError_t ce = cudaMemsetAsync(weights, 0, rows * weights_stride * sizeof(float), st);
     if (ce != cudaSuccess) return fail_cuda(ce, "pa_prefill_weights memset");
     if (total_tokens == 0 || max_seq_len == 0) return PA_OK;
+    mark_called(dtype == PA_F32 ? kPrefillSimt : kPrefill);
     if (dtype == PA_F32) {
         ce = pa::launch_prefill_weights_simt(p, st);
     } else {
@@ -1124,6 +1143,7 @@ int pa_evict(void* k_cache, void* v_cache, const int32_t* block_tables,
     p.row_vecs = cache->head_dim * elem_bytes(cache->dtype) / 16;
     p.budget = budget;
     p.recent = recent;
+    mark_called(kEvict);
     cudaError_t e = pa::launch_evict(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : fail_cuda(e, "pa_evict launch");
 }
@@ -1137,21 +1157,14 @@ int pa_sync_check(void* stream) {
     if ((e = pa::read_status_copy(&a, true)) != cudaSuccess ||
         (e = pa::read_status_tma(&b, true)) != cudaSuccess)
         return fail_cuda(e, "pa_sync_check: status word");
-    // the calls around decode: rotary append and eviction beside the copies, prompt
-    // attention beside decode
-    unsigned x = 0;
-    if ((e = pa::read_status_rope(&x, true)) != cudaSuccess)
-        return fail_cuda(e, "pa_sync_check: status word");
-    a |= x;
-    if ((e = pa::read_status_evict(&x, true)) != cudaSuccess)
-        return fail_cuda(e, "pa_sync_check: status word");
-    a |= x;
-    if ((e = pa::read_status_prefill(&x, true)) != cudaSuccess)
-        return fail_cuda(e, "pa_sync_check: status word");
-    b |= x;
-    if ((e = pa::read_status_prefill_simt(&x, true)) != cudaSuccess)
-        return fail_cuda(e, "pa_sync_check: status word");
-    b |= x;
+    // the calls around decode, where the process made them: rotary append and eviction beside the
+    // copies, prompt attention beside decode
+    for (const AroundDecode& w : g_around_decode) {
+        if (!w.called.load(std::memory_order_acquire)) continue;
+        unsigned x = 0;
+        if ((e = w.read(&x, true)) != cudaSuccess) return fail_cuda(e, "pa_sync_check: status word");
+        (w.beside_copies ? a : b) |= x;
+    }
     if ((a | b) & pa::kStatusSmemAlign)
         return fail(PA_ERR_CUDA, "a decode kernel found its shared memory misaligned and did not run");
     if ((a | b) & pa::kStatusTimeout)
