@@ -72,7 +72,8 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.f;
 
 // Bounded wait; gives up at once when another role already gave up.
-__device__ __forceinline__ bool wait_or_dead(volatile int* dead, uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_or_dead(volatile int* dead, uint32_t bar, uint32_t parity,
+                                             uint64_t limit_ns = kWaitLimitNs) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     for (;;) {
@@ -80,7 +81,7 @@ __device__ __forceinline__ bool wait_or_dead(volatile int* dead, uint32_t bar, u
         for (int i = 0; i < 64; ++i)
             if (mbar_try_wait(bar, parity)) return true;
         if (*dead != 0) return false;
-        if (global_timer_ns() - t0 > kWaitLimitNs) {
+        if (global_timer_ns() - t0 > limit_ns) {
             atomicOr(&s_status_prefill, kStatusTimeout);
             *dead = 1;
             return false;
@@ -175,6 +176,10 @@ constexpr int kNothing = -1, kEnd = -2;
 
 // Shared-memory places of the hand-over of items: four slots in turn.
 constexpr int kSlots = 4;
+// The walker runs ahead of the others and may wait for a slot as long as an item takes (weights
+// of 866 heads and 113K queries: over a second). A role that cannot go on gives up after
+// kWaitLimitNs and ends this wait with it.
+constexpr uint64_t kItemLimitNs = 100 * kWaitLimitNs;
 struct ItemBars {
     uint32_t full, empty, answer;  // [kSlots], [kSlots], and of the launch control's answer
     volatile int* slots;           // [kSlots][8]
@@ -224,7 +229,8 @@ __device__ __forceinline__ void walk_items(const PrefillParams& p, int heads, co
         }
         const int slot = n % kSlots;
         if (n >= kSlots &&
-            !__all_sync(0xffffffffu, wait_or_dead(dead, ib.empty + 8 * slot, ((n / kSlots) & 1) ^ 1)))
+            !__all_sync(0xffffffffu, wait_or_dead(dead, ib.empty + 8 * slot, ((n / kSlots) & 1) ^ 1,
+                                                      kItemLimitNs)))
             return;
         if (lane == 0) {
             volatile int* d = ib.slots + 8 * slot;
