@@ -539,6 +539,11 @@ typedef struct pa_rope_desc {
  * formed in fp32. num_heads >= 0: with 0 only k and v
  * are appended (q and q_out may then be NULL).
  *
+ * Rotated keys for pa_prefill. With q pointing at the heads of q and k together, as they lie
+ * in a packed projection, and num_heads their number, q_out holds the turned q and, behind them
+ * in each token, the turned k: both are rows as pa_prefill and pa_prefill_weights take them (the
+ * token stride is num_heads * head_dim), also where the pool itself holds codes.
+ *
  * pa_rope_append_quant — the same into a quantised cache: q, k, v and q_out bf16, each
  * k and v element stored as the code of (its unrounded fp32 value) / scale[kv head].
  */

@@ -710,7 +710,9 @@ def pa_rope_append(q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, ro
     """q_out = q turned by its positions; k turned likewise and v as it is go to their
     cache slots (int64; <0: padding, not stored). q, k, v [T][heads][head_dim] may be
     slices of a packed projection; positions int32 [num_axes][T]; ``rope`` from
-    ``rope_desc``."""
+    ``rope_desc``. With the heads of q and k together as q ([T][num_heads + num_kv_heads][D]
+    of a packed projection), q_out also holds the rotated keys behind the queries, and
+    its slices are what pa_prefill and pa_prefill_weights take as q and k."""
     _rope_call(load_library().pa_rope_append, (), q_out, q, k, v, positions, slot_mapping, k_cache,
                v_cache, rope, k_cache.dtype, stream)
 
