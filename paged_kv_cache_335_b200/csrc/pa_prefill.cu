@@ -24,7 +24,7 @@
 //     not finite, and the rows behind the prompt, before the tensor core reads
 //     them: a masked weight is 0, and 0 x infinity would not be. The epilogue adds the
 //     elements so taken out to the rows that attend to them.
-// The weights are 2^(score - m) with m a reference that moves only when a row's
+// The weights are 2^(score - m) with m a reference that moves (a published idea) only when a row's
 // maximum exceeds it by more than 2^kRescaleLog2 (numerator and denominator share it, so
 // the result is the exact softmax); O is then rescaled in TMEM by its row's own
 // threads. What a row does depends on its own scores alone. P is rounded to bf16 for
@@ -45,11 +45,12 @@
 // key tile and row block at head_dim 128), the exponential unit (16 per cycle and SM:
 // 1024 cycles per 128 x 128 weights) and, in between, the chain S -> softmax -> P V ->
 // next S of a row block (about 1500 + 512 + 512 + 380 cycles), which the other row
-// block only partly covers. 16K tokens of 64/8 heads: 3.42 to 3.53 ms = 1250 to 1286
-// TFLOP/s in rows of five (power-capped clock), tensor pipe 54% active at 4K. A product of
-// 64 keys costs the cycles of one of 128, so smaller steps with two score buffers were
-// slower (4.4 ms).
-// Bound of the weights: the exponential unit (73% active at 4K).
+// block only partly covers. 16K tokens of 64/8 heads, tensor pipe 55% active at 4K: 3.56 ms =
+// 1235 TFLOP/s in a short row of launches, 4.0 ms = 1100 in a long one, whose clock
+// the power cap holds lower. A product of 64 keys costs the cycles of one of 128, so smaller
+// steps with two score buffers were slower (4.4 ms against 4.0 at the time).
+// Bound of the weights: the exponential unit (71% active at 4K); 8K tokens of 64/8 heads 0.69 to
+// 0.74 ms.
 #include <math.h>
 
 #include <algorithm>
